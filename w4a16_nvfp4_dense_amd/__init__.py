@@ -37,6 +37,17 @@ and the W4A4 prefill arm over MXFP4 operands (``include/ffn_w4a4.h``):
 * :func:`w4a4_down_gemm`  -- ``ffn_w4a4_down_gemm`` (the down projection on 4 bits)
 * :func:`w4a4_forward_fp4` -- ``ffn_w4a4_forward_fp4`` (all three projections on 4 bits)
 * :func:`w4a4_fp4_workspace_bytes` -- ``ffn_w4a4_fp4_workspace_bytes``
+
+and the int8 (W8A8) arm with the operators around it (``include/ffn_int8.h``):
+
+* :func:`int8_rmsnorm`   -- ``ffn_int8_rmsnorm`` norm of x + residual -> int8 codes, scales
+* :func:`int8_quantize`  -- ``ffn_int8_quantize`` rows -> int8 codes, scales
+* :func:`int8_quantize_weight` -- the same as an :class:`Int8DeviceWeight`
+* :func:`int8_prepare_weight`  -- ``ffn_int8_prepare_weight`` NVFP4 -> int8 (once)
+* :func:`int8_gemm`      -- ``ffn_int8_gemm`` the product with token and channel scales
+* :func:`int8_dual_gemm` -- ``ffn_int8_dual_gemm`` act(gate) * up -> int8 codes, scales
+* :func:`int8_forward`   -- ``ffn_int8_forward`` the whole FFN
+* :func:`int8_gemm_workspace_bytes`, :func:`int8_workspace_bytes`
 """
 from __future__ import annotations
 
@@ -50,6 +61,7 @@ LIB_PATH = os.path.join(PKG_DIR, "lib", "libffn_nvfp4.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_nvfp4.h")
 FP8_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_fp8.h")
 W4A4_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_w4a4.h")
+INT8_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_int8.h")
 DIAG_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_diag.h")
 
 ACT_SILU = 0
@@ -90,6 +102,12 @@ class MxWeightStruct(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("scale2", ctypes.c_float)]
 
 
+class Int8WeightStruct(ctypes.Structure):
+    """ffn_int8_weight: device codes, device fp32 scale for each row."""
+
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _P = ctypes.c_void_p
@@ -97,6 +115,7 @@ _I = ctypes.c_int
 _WP = ctypes.POINTER(WeightStruct)
 _FP = ctypes.POINTER(Fp8WeightStruct)
 _MP = ctypes.POINTER(MxWeightStruct)
+_QP = ctypes.POINTER(Int8WeightStruct)
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -150,6 +169,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ffn_w4a4_down_gemm.argtypes = [_P, _I, _I, _I, _MP, _P, _P, ctypes.c_size_t, _P]
     lib.ffn_w4a4_forward_fp4.restype = _I
     lib.ffn_w4a4_forward_fp4.argtypes = [_P, _I, _I, _I, _MP, _MP, _MP, _I, _P, ctypes.c_size_t, _P, _P]
+    lib.ffn_int8_rmsnorm.restype = _I
+    lib.ffn_int8_rmsnorm.argtypes = [_P, _P, _P, _I, _I, _I, _I, ctypes.c_float, ctypes.c_float, _P, _P, _P, _P, _P]
+    lib.ffn_int8_quantize.restype = _I
+    lib.ffn_int8_quantize.argtypes = [_P, _I, _I, _I, _P, _P, _P]
+    lib.ffn_int8_prepare_weight.restype = _I
+    lib.ffn_int8_prepare_weight.argtypes = [_WP, _I, _I, _P, _P, _P]
+    lib.ffn_int8_gemm_workspace_bytes.restype = ctypes.c_size_t
+    lib.ffn_int8_gemm_workspace_bytes.argtypes = [_I, _I, _I]
+    lib.ffn_int8_gemm.restype = _I
+    lib.ffn_int8_gemm.argtypes = [_P, _P, _I, _I, _I, _QP, _P, _I, _P, _P, ctypes.c_size_t, _P]
+    lib.ffn_int8_workspace_bytes.restype = ctypes.c_size_t
+    lib.ffn_int8_workspace_bytes.argtypes = [_I, _I, _I]
+    lib.ffn_int8_dual_gemm.restype = _I
+    lib.ffn_int8_dual_gemm.argtypes = [_P, _P, _I, _I, _I, _QP, _QP, _I, _P, _P, _P, ctypes.c_size_t, _P]
+    lib.ffn_int8_forward.restype = _I
+    lib.ffn_int8_forward.argtypes = [_P, _P, _I, _I, _I, _QP, _QP, _QP, _I, _I, _P, ctypes.c_size_t, _P, _P]
     _lib = lib
     return lib
 
@@ -159,7 +194,7 @@ def header_functions(path: str = HEADER_PATH) -> Sequence[str]:
     import re
     text = open(path).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(ffn_(?:nvfp4|fp8|w4a4|diag)_[a-z_0-9]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(ffn_(?:nvfp4|fp8|w4a4|int8|diag)_[a-z_0-9]+)\s*\(", text)))
 
 
 def version() -> int:
@@ -681,6 +716,272 @@ def w4a4_forward_fp4(x, gate: MxDeviceWeight, up: MxDeviceWeight, down: MxDevice
                                      int(act), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                      out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_w4a4_forward_fp4")
+    _record(stream, *fresh)
+    return out
+
+
+# ------------------------------------------------------------ int8 (W8A8)
+
+
+@dataclasses.dataclass
+class Int8DeviceWeight:
+    """An int8 weight on the GPU: codes int8 [rows, cols] and one fp32 scale
+    for each row (output channel) [rows]."""
+
+    codes: "object"
+    scales: "object"
+
+    @property
+    def rows(self) -> int:
+        return int(self.codes.shape[0])
+
+    @property
+    def cols(self) -> int:
+        return int(self.codes.shape[1])
+
+    def struct(self) -> Int8WeightStruct:
+        return Int8WeightStruct(self.codes.data_ptr(), self.scales.data_ptr())
+
+    @classmethod
+    def from_host(cls, w, device="cuda") -> "Int8DeviceWeight":
+        """From an object with numpy ``codes`` and ``scales``."""
+        import torch
+        return cls(torch.from_numpy(w.codes).to(device), torch.from_numpy(w.scales).to(device))
+
+
+def _int8_dtype(dtype, name: str) -> int:
+    """ffn_int8_dtype of a torch type."""
+    import torch
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
+    return code
+
+
+def _check_int8_weight(w: Int8DeviceWeight, rows: int, cols: int, name: str, device) -> None:
+    """An int8 weight of logical shape [rows, cols] on the device of the call."""
+    import torch
+    _check_tensor(w.codes, torch.int8, (rows, cols), f"{name}.codes", device)
+    _check_tensor(w.scales, torch.float32, (rows,), f"{name}.scales", device)
+
+
+def _check_workspace(workspace, device) -> None:
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
+def int8_rmsnorm(x, weight, eps: float = 1e-6, residual=None, weight_offset: float = 0.0, codes=None, scales=None,
+                 sum_out=None, y_out=None, stream=None):
+    """(codes int8 [M, K], scales fp32 [M], t) of the root-mean-square norm of
+    t = x + residual: the int8 rows of t / sqrt(mean t^2 + eps) *
+    (weight_offset + weight). t (x's type, the new residual stream) is None
+    without a residual, unless ``sum_out`` is given; ``sum_out`` may be x or
+    residual. ``y_out`` (x's type), if given, receives the norm itself, for
+    arms that take real activations."""
+    import torch
+    M, K = x.shape
+    dtype, wdtype = _int8_dtype(x.dtype, "x"), _int8_dtype(weight.dtype, "weight")
+    dev = x.device
+    _check_tensor(x, x.dtype, (M, K), "x")
+    _check_tensor(weight, weight.dtype, (K,), "weight", dev)
+    if residual is not None:
+        _check_tensor(residual, x.dtype, (M, K), "residual", dev)
+    fresh = []
+    if codes is None:
+        codes = torch.empty((M, K), dtype=torch.int8, device=dev)
+        fresh.append(codes)
+    else:
+        _check_tensor(codes, torch.int8, (M, K), "codes", dev)
+    if scales is None:
+        scales = torch.empty(M, dtype=torch.float32, device=dev)
+        fresh.append(scales)
+    else:
+        _check_tensor(scales, torch.float32, (M,), "scales", dev)
+    if sum_out is None:
+        if residual is not None:
+            sum_out = torch.empty((M, K), dtype=x.dtype, device=dev)
+            fresh.append(sum_out)
+    else:
+        _check_tensor(sum_out, x.dtype, (M, K), "sum_out", dev)
+    if y_out is not None:
+        _check_tensor(y_out, x.dtype, (M, K), "y_out", dev)
+    rc = load().ffn_int8_rmsnorm(x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(),
+                                 M, K, dtype, wdtype, eps, weight_offset, codes.data_ptr(), scales.data_ptr(),
+                                 None if sum_out is None else sum_out.data_ptr(),
+                                 None if y_out is None else y_out.data_ptr(), _stream_handle(stream))
+    _check(rc, "ffn_int8_rmsnorm")
+    _record(stream, *fresh)
+    return codes, scales, sum_out
+
+
+def int8_quantize(x, codes=None, scales=None, stream=None):
+    """(codes int8 [rows, cols], scales fp32 [rows]) of the rows of x."""
+    import torch
+    rows, cols = x.shape
+    dtype = _int8_dtype(x.dtype, "x")
+    dev = x.device
+    _check_tensor(x, x.dtype, (rows, cols), "x")
+    fresh = []
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+        fresh.append(codes)
+    else:
+        _check_tensor(codes, torch.int8, (rows, cols), "codes", dev)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+        fresh.append(scales)
+    else:
+        _check_tensor(scales, torch.float32, (rows,), "scales", dev)
+    rc = load().ffn_int8_quantize(x.data_ptr(), rows, cols, dtype, codes.data_ptr(), scales.data_ptr(),
+                                  _stream_handle(stream))
+    _check(rc, "ffn_int8_quantize")
+    _record(stream, *fresh)
+    return codes, scales
+
+
+def int8_quantize_weight(w, stream=None) -> Int8DeviceWeight:
+    """:func:`int8_quantize` of a weight [N, K] as an Int8DeviceWeight (asynchronous)."""
+    return Int8DeviceWeight(*int8_quantize(w, stream=stream))
+
+
+def int8_prepare_weight(w: DeviceWeight, stream=None) -> Int8DeviceWeight:
+    """An NVFP4 weight as int8 rows on the GPU (asynchronous)."""
+    import torch
+    rows, cols = w.rows, w.cols
+    dev = w.codes.device
+    _check_nvfp4_weight(w, rows, cols, "w", dev)
+    codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    st = w.struct()
+    rc = load().ffn_int8_prepare_weight(ctypes.byref(st), rows, cols, codes.data_ptr(), scales.data_ptr(),
+                                        _stream_handle(stream))
+    _check(rc, "ffn_int8_prepare_weight")
+    _record(stream, codes, scales)
+    return Int8DeviceWeight(codes, scales)
+
+
+def int8_gemm_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(load().ffn_int8_gemm_workspace_bytes(int(M), int(K), int(N)))
+
+
+def int8_gemm(xq, xs, w: Int8DeviceWeight, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
+    """out[M, N] = xs * w.scales * (xq . w.codes) + bias in ``out_dtype`` (the
+    type of ``out`` if that is given, else bfloat16); xq int8 [M, K], xs fp32 [M]."""
+    import torch
+    M, K = xq.shape
+    N = w.rows
+    dev = xq.device
+    _check_tensor(xq, torch.int8, (M, K), "xq")
+    _check_tensor(xs, torch.float32, (M,), "xs", dev)
+    _check_int8_weight(w, N, K, "w", dev)
+    if bias is not None:
+        _check_tensor(bias, torch.float32, (N,), "bias", dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    dtype = _int8_dtype(out_dtype, "out")
+    fresh = []
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        fresh.append(out)
+    else:
+        _check_tensor(out, out_dtype, (M, N), "out", dev)
+    lib = load()
+    need = lib.ffn_int8_gemm_workspace_bytes(M, K, N)
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            fresh.append(workspace)
+    else:
+        _check_workspace(workspace, dev)
+    st = w.struct()
+    rc = lib.ffn_int8_gemm(xq.data_ptr(), xs.data_ptr(), M, K, N, ctypes.byref(st),
+                           None if bias is None else bias.data_ptr(), dtype, out.data_ptr(),
+                           None if workspace is None else workspace.data_ptr(),
+                           0 if workspace is None else workspace.numel() * workspace.element_size(),
+                           _stream_handle(stream))
+    _check(rc, "ffn_int8_gemm")
+    _record(stream, *fresh)
+    return out
+
+
+def int8_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(load().ffn_int8_workspace_bytes(int(M), int(K), int(N)))
+
+
+def int8_dual_gemm(xq, xs, gate: Int8DeviceWeight, up: Int8DeviceWeight, act: int = ACT_SILU, hq=None, hs=None,
+                   workspace=None, stream=None):
+    """(hq int8 [M, N], hs fp32 [M]): the int8 rows of act(W_g x) * (W_u x)."""
+    import torch
+    M, K = xq.shape
+    N = gate.rows
+    dev = xq.device
+    _check_tensor(xq, torch.int8, (M, K), "xq")
+    _check_tensor(xs, torch.float32, (M,), "xs", dev)
+    _check_int8_weight(gate, N, K, "gate", dev)
+    _check_int8_weight(up, N, K, "up", dev)
+    fresh = []
+    if hq is None:
+        hq = torch.empty((M, N), dtype=torch.int8, device=dev)
+        fresh.append(hq)
+    else:
+        _check_tensor(hq, torch.int8, (M, N), "hq", dev)
+    if hs is None:
+        hs = torch.empty(M, dtype=torch.float32, device=dev)
+        fresh.append(hs)
+    else:
+        _check_tensor(hs, torch.float32, (M,), "hs", dev)
+    lib = load()
+    need = lib.ffn_int8_workspace_bytes(M, K, N)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        fresh.append(workspace)
+    else:
+        _check_workspace(workspace, dev)
+    g, u = gate.struct(), up.struct()
+    rc = lib.ffn_int8_dual_gemm(xq.data_ptr(), xs.data_ptr(), M, K, N, ctypes.byref(g), ctypes.byref(u), int(act),
+                                hq.data_ptr(), hs.data_ptr(), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check(rc, "ffn_int8_dual_gemm")
+    _record(stream, *fresh)
+    return hq, hs
+
+
+def int8_forward(xq, xs, gate: Int8DeviceWeight, up: Int8DeviceWeight, down: Int8DeviceWeight, act: int = ACT_SILU,
+                 out_dtype=None, out=None, workspace=None, stream=None):
+    """out[M, K] = W_d q(act(W_g x) * (W_u x)) over int8 weights, for x as
+    int8 rows (xq int8 [M, K], xs fp32 [M]); ``out_dtype`` as :func:`int8_gemm`."""
+    import torch
+    M, K = xq.shape
+    N = gate.rows
+    dev = xq.device
+    _check_tensor(xq, torch.int8, (M, K), "xq")
+    _check_tensor(xs, torch.float32, (M,), "xs", dev)
+    _check_int8_weight(gate, N, K, "gate", dev)
+    _check_int8_weight(up, N, K, "up", dev)
+    _check_int8_weight(down, K, N, "down", dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    dtype = _int8_dtype(out_dtype, "out")
+    fresh = []
+    if out is None:
+        out = torch.empty((M, K), dtype=out_dtype, device=dev)
+        fresh.append(out)
+    else:
+        _check_tensor(out, out_dtype, (M, K), "out", dev)
+    lib = load()
+    need = lib.ffn_int8_workspace_bytes(M, K, N)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        fresh.append(workspace)
+    else:
+        _check_workspace(workspace, dev)
+    g, u, d = gate.struct(), up.struct(), down.struct()
+    rc = lib.ffn_int8_forward(xq.data_ptr(), xs.data_ptr(), M, K, N, ctypes.byref(g), ctypes.byref(u),
+                              ctypes.byref(d), int(act), dtype, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), out.data_ptr(), _stream_handle(stream))
+    _check(rc, "ffn_int8_forward")
     _record(stream, *fresh)
     return out
 
