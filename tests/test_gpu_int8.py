@@ -272,6 +272,50 @@ def test_gemm_nan_scale_stays_in_its_row(M):
     assert np.array_equal(out[keep], ref[keep])
 
 
+@pytest.mark.parametrize("M,K,N,dtype,bias", [
+    (1024, 272, 10250, "f32", True),    # 256 x 256 tiles, fewer than compute units, a short last stage
+    (1792, 144, 19001, "bf16", False),  # two rounds of them and a shared rest, ragged channels
+    (2300, 128, 20480, "f16", True),    # one stage a tile, ragged tokens
+    (250, 400, 16500, "f32", False),    # 256 x 128 tiles
+    (256, 2064, 17408, "bf16", True),
+    (1, 5120, 30000, "f32", True),      # weights read non-temporally
+    (40, 4112, 33333, "bf16", False),
+    (64, 8208, 16500, "f32", False),
+    (37, 2064, 5000, "f32", True),      # 64 x 64 tiles
+    (700, 1040, 3000, "f16", False),
+])
+def test_gemm_large(M, K, N, dtype, bias):
+    """Every tile shape at sizes with several rounds of tiles, shared tiles and
+    ragged ends, bit for bit: integer sums in float64 on the GPU are exact, and
+    torch's fp32 products and sums round as the chain does."""
+    g = torch.Generator(device="cuda").manual_seed(M + K + N)
+    xq = torch.randint(-128, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    xs = torch.rand(M, generator=g, device="cuda") / 64
+    ws = torch.rand(N, generator=g, device="cuda") / 64
+    b = torch.randn(N, generator=g, device="cuda") if bias else None
+    ref = (xq.double() @ wq.double().t().contiguous()).float() * xs[:, None] * ws
+    if bias:
+        ref = ref + b
+    workspace = torch.full((max(16, ffn.int8_gemm_workspace_bytes(M, K, N)),), 0xA5, dtype=torch.uint8, device="cuda")
+    for _ in range(2):  # the second call finds what the first one left
+        out = ffn.int8_gemm(xq, xs, ffn.Int8DeviceWeight(wq, ws), bias=b, out_dtype=TORCH[dtype], workspace=workspace)
+        assert same_bits(out, ref.to(TORCH[dtype]))
+
+
+@pytest.mark.parametrize("M,K,N,act", [(1024, 144, 5136, 0), (1300, 256, 10240, 1), (250, 272, 8256, 0), (500, 528, 1040, 1)])
+def test_dual_large(M, K, N, act):
+    """The gated product on the tile shapes of many tokens: the same bits as on
+    those of few (which the tests below hold against 64 bits)."""
+    xq, xs, gate, up, down = _config(M, K, N, M + N)
+    hq, hs = ffn.int8_dual_gemm(xq, xs, gate, up, act)
+    for lo in range(0, M, 61):
+        q, s = ffn.int8_dual_gemm(xq[lo:lo + 3], xs[lo:lo + 3], gate, up, act)
+        assert same_bits(q, hq[lo:lo + 3]) and same_bits(s, hs[lo:lo + 3])
+    out = ffn.int8_forward(xq, xs, gate, up, down, act)
+    assert same_bits(out, ffn.int8_gemm(hq, hs, down))
+
+
 @pytest.mark.parametrize("K,N", [(5120, 17408), (17408, 5120), (1040, 531)])
 def test_gemm_rows_do_not_depend_on_the_batch(K, N):
     """Row m of every batch has the bits of a call on that row alone."""

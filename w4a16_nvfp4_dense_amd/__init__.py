@@ -242,8 +242,11 @@ class DeviceWeight:
 
 
 def _stream_handle(stream) -> int:
-    import torch
     if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:  # the same handle without building a Stream object
+            return raw(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -253,9 +256,9 @@ def _record(stream, *tensors) -> None:
     pool; when the call was enqueued on another stream, mark them as used
     there so the caching allocator cannot hand their memory out again before
     that stream's kernels are done."""
-    import torch
     if stream is None:
         return
+    import torch
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     if int(s.cuda_stream) == int(torch.cuda.current_stream().cuda_stream):
         return
@@ -265,7 +268,10 @@ def _record(stream, *tensors) -> None:
 
 
 def _check_tensor(t, dtype, shape, name, device=None):
-    import torch
+    dev = t.device
+    if (t.dtype == dtype and t.shape == shape and t.is_contiguous()
+            and dev.type == "cuda" and (device is None or dev == device)):
+        return
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a GPU tensor")
     if device is not None and t.device != device:
@@ -749,10 +755,15 @@ class Int8DeviceWeight:
         return cls(torch.from_numpy(w.codes).to(device), torch.from_numpy(w.scales).to(device))
 
 
+_INT8_DTYPES: dict = {}  # torch type -> ffn_int8_dtype, filled at first use
+
+
 def _int8_dtype(dtype, name: str) -> int:
     """ffn_int8_dtype of a torch type."""
-    import torch
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    if not _INT8_DTYPES:
+        import torch
+        _INT8_DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _INT8_DTYPES.get(dtype)
     if code is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
     return code
@@ -761,6 +772,10 @@ def _int8_dtype(dtype, name: str) -> int:
 def _check_int8_weight(w: Int8DeviceWeight, rows: int, cols: int, name: str, device) -> None:
     """An int8 weight of logical shape [rows, cols] on the device of the call."""
     import torch
+    c, s = w.codes, w.scales
+    if (c.dtype == torch.int8 and c.shape == (rows, cols) and c.is_contiguous() and c.device == device
+            and s.dtype == torch.float32 and s.shape == (rows,) and s.is_contiguous() and s.device == device):
+        return
     _check_tensor(w.codes, torch.int8, (rows, cols), f"{name}.codes", device)
     _check_tensor(w.scales, torch.float32, (rows,), f"{name}.scales", device)
 

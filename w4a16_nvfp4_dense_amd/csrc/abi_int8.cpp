@@ -3,6 +3,7 @@
 // no HIP call is made when a check fails.
 #include "ffn_int8.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -76,29 +77,33 @@ ffn::Int8Out out_kind(int dtype)
     return dtype == FFN_INT8_BF16 ? ffn::I8_BF16 : dtype == FFN_INT8_F16 ? ffn::I8_F16 : ffn::I8_F32;
 }
 
-// The workspace of the gated FFN: h fp32 [M, N], its codes [M, N] and scales [M].
+// The workspace of the gated FFN: h fp32 [M, N], its codes [M, N] and scales
+// [M], then what the split products need (one at a time).
 struct Workspace {
-    size_t h, codes, scales, total;
+    size_t h, codes, scales, split, total;
 };
 
-Workspace layout(int M, int N)
+Workspace layout(int M, int K, int N)
 {
     Workspace w;
     const size_t e = static_cast<size_t>(M) * static_cast<size_t>(N);
     w.h = 0;
     w.codes = round256(4 * e);
     w.scales = w.codes + round256(e);
-    w.total = w.scales + round256(4 * static_cast<size_t>(M));
+    w.split = w.scales + round256(4 * static_cast<size_t>(M));
+    w.total = w.split + std::max(ffn::int8_gemm_workspace(M, K, N, ffn::I8_H_SILU),
+                                 ffn::int8_gemm_workspace(M, N, K, ffn::I8_BF16));
     return w;
 }
 
 // h = act(gate) * up in fp32, then its int8 rows.
 hipError_t dual(const int8_t *xq, const float *xs, int M, int K, int N, const ffn_int8_weight *gate,
-                const ffn_int8_weight *up, int act, int8_t *hq, float *hs, float *h, hipStream_t stream)
+                const ffn_int8_weight *up, int act, int8_t *hq, float *hs, float *h, void *split,
+                hipStream_t stream)
 {
     const ffn::Int8GemmArgs a{xq, xs, gate->codes, up->codes, gate->scales, up->scales, nullptr, h, M, K, N};
     const hipError_t e =
-        ffn::launch_int8_gemm(a, act == FFN_NVFP4_ACT_SILU ? ffn::I8_H_SILU : ffn::I8_H_GELU, stream);
+        ffn::launch_int8_gemm(a, act == FFN_NVFP4_ACT_SILU ? ffn::I8_H_SILU : ffn::I8_H_GELU, split, stream);
     if (e != hipSuccess)
         return e;
     ffn::Int8RowsArgs r{};
@@ -176,15 +181,15 @@ int ffn_int8_prepare_weight(const ffn_nvfp4_weight *w, int rows, int cols, int8_
         return FFN_NVFP4_ERR_SHAPE;
     if (!std::isfinite(w->scale2))
         return FFN_NVFP4_ERR_SCALE2;
-    return launch_status(ffn::launch_int8_requant(w->codes, w->scales, w->scale2, rows, cols, codes, scales, stream));
+    return launch_status(
+        ffn::launch_int8_requant(w->codes, w->scales, w->scale2, rows, cols, codes, scales, stream));
 }
 
 size_t ffn_int8_gemm_workspace_bytes(int M, int K, int N)
 {
-    (void)M;
-    (void)K;
-    (void)N;
-    return 0;
+    if (M == 0 || check_gemm(M, K, N) != FFN_NVFP4_OK)
+        return 0;
+    return ffn::int8_gemm_workspace(M, K, N, ffn::I8_BF16);
 }
 
 int ffn_int8_gemm(const int8_t *xq, const float *xs, int M, int K, int N, const ffn_int8_weight *w,
@@ -206,14 +211,14 @@ int ffn_int8_gemm(const int8_t *xq, const float *xs, int M, int K, int N, const 
     if (workspace_bytes < need)
         return FFN_NVFP4_ERR_WORKSPACE;
     const ffn::Int8GemmArgs a{xq, xs, w->codes, nullptr, w->scales, nullptr, bias, out, M, K, N};
-    return launch_status(ffn::launch_int8_gemm(a, out_kind(out_dtype), stream));
+    return launch_status(ffn::launch_int8_gemm(a, out_kind(out_dtype), workspace, stream));
 }
 
 size_t ffn_int8_workspace_bytes(int M, int K, int N)
 {
     if (M == 0 || check_ffn(M, K, N) != FFN_NVFP4_OK)
         return 0;
-    return layout(M, N).total;
+    return layout(M, K, N).total;
 }
 
 int ffn_int8_dual_gemm(const int8_t *xq, const float *xs, int M, int K, int N, const ffn_int8_weight *gate,
@@ -233,7 +238,9 @@ int ffn_int8_dual_gemm(const int8_t *xq, const float *xs, int M, int K, int N, c
         return FFN_NVFP4_ERR_ALIGN;
     if (workspace_bytes < ffn_int8_workspace_bytes(M, K, N))
         return FFN_NVFP4_ERR_WORKSPACE;
-    return launch_status(dual(xq, xs, M, K, N, gate, up, act, hq, hs, static_cast<float *>(workspace), stream));
+    char *ws = static_cast<char *>(workspace);
+    return launch_status(dual(xq, xs, M, K, N, gate, up, act, hq, hs, reinterpret_cast<float *>(ws),
+                              ws + layout(M, K, N).split, stream));
 }
 
 int ffn_int8_forward(const int8_t *xq, const float *xs, int M, int K, int N, const ffn_int8_weight *gate,
@@ -254,15 +261,16 @@ int ffn_int8_forward(const int8_t *xq, const float *xs, int M, int K, int N, con
         return FFN_NVFP4_ERR_ALIGN;
     if (workspace_bytes < ffn_int8_workspace_bytes(M, K, N))
         return FFN_NVFP4_ERR_WORKSPACE;
-    const Workspace w = layout(M, N);
+    const Workspace w = layout(M, K, N);
     char *ws = static_cast<char *>(workspace);
     int8_t *hq = reinterpret_cast<int8_t *>(ws + w.codes);
     float *hs = reinterpret_cast<float *>(ws + w.scales);
-    const hipError_t e = dual(xq, xs, M, K, N, gate, up, act, hq, hs, reinterpret_cast<float *>(ws + w.h), stream);
+    const hipError_t e = dual(xq, xs, M, K, N, gate, up, act, hq, hs, reinterpret_cast<float *>(ws + w.h),
+                              ws + w.split, stream);
     if (e != hipSuccess)
         return FFN_NVFP4_ERR_LAUNCH;
     const ffn::Int8GemmArgs a{hq, hs, down->codes, nullptr, down->scales, nullptr, nullptr, out, M, N, K};
-    return launch_status(ffn::launch_int8_gemm(a, out_kind(out_dtype), stream));
+    return launch_status(ffn::launch_int8_gemm(a, out_kind(out_dtype), ws + w.split, stream));
 }
 
 }  // extern "C"

@@ -48,15 +48,9 @@ constexpr bool int8_two_weights(int out)
     return out == I8_H_SILU || out == I8_H_GELU;
 }
 
-// Few tokens (M <= kInt8SkinnyTokens): weights streamed to registers.
-constexpr int kInt8SkinnyTokens = 64;
-hipError_t launch_int8_skinny(const Int8GemmArgs &a, Int8Out out, hipStream_t stream);
-// Any M: tiles of both operands in LDS.
-hipError_t launch_int8_tile(const Int8GemmArgs &a, Int8Out out, hipStream_t stream);
-
-inline hipError_t launch_int8_gemm(const Int8GemmArgs &a, Int8Out out, hipStream_t stream)
-{
-    return a.M <= kInt8SkinnyTokens ? launch_int8_skinny(a, out, stream) : launch_int8_tile(a, out, stream);
-}
+// The product (int8_tile.hip). `workspace` holds int8_gemm_workspace(...) bytes
+// (any contents): what workgroups that share a tile exchange.
+hipError_t launch_int8_gemm(const Int8GemmArgs &a, Int8Out out, void *workspace, hipStream_t stream);
+size_t int8_gemm_workspace(int M, int K, int N, Int8Out out);
 
 }  // namespace ffn

@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "int8.h"
 #include "nvfp4_device.h"
 
@@ -79,66 +81,46 @@ __device__ __forceinline__ float int8_gated(float g, float u)
     return g * __builtin_amdgcn_rcpf(1.0f + __expf(z)) * u;
 }
 
-// Four results of channels n .. n + 3 of token m (those below N), in the
-// output's type: one vector store where the row length keeps it aligned.
-template <int OUT>
-__device__ __forceinline__ void int8_store4(const Int8GemmArgs &a, int m, int n, const float (&v)[4])
+// C results of channels n .. n + C - 1 of token m (those below N), n a
+// multiple of C, in the output's type: one store where the row length keeps it
+// aligned.
+template <int OUT, int C>
+__device__ __forceinline__ void int8_store(const Int8GemmArgs &a, int m, int n, const float (&v)[C])
 {
     const size_t at = static_cast<size_t>(m) * a.N + n;
-    const bool whole = (a.N & 3) == 0;  // n is a multiple of 4
+    const bool whole = a.N % C == 0;
     if constexpr (OUT == I8_BF16) {
         uint16_t *o = static_cast<uint16_t *>(a.out) + at;
-        if (whole) {
-            *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        if (C > 1 && whole) {
+            typedef uint32_t pairs __attribute__((ext_vector_type(C > 1 ? C / 2 : 1)));
+            pairs p;
+#pragma unroll
+            for (int i = 0; i < C / 2; ++i)
+                p[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            *reinterpret_cast<pairs *>(o) = p;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < C; ++i)
                 if (n + i < a.N)
                     o[i] = to_bf16_bits(v[i]);
         }
-    } else if constexpr (OUT == I8_F16) {
-        _Float16 *o = static_cast<_Float16 *>(a.out) + at;
-        if (whole) {
-            typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-            *reinterpret_cast<f16x4 *>(o) = f16x4{static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1]),
-                                                  static_cast<_Float16>(v[2]), static_cast<_Float16>(v[3])};
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n + i < a.N)
-                    o[i] = static_cast<_Float16>(v[i]);
-        }
     } else {
-        float *o = static_cast<float *>(a.out) + at;
+        typedef typename std::conditional<OUT == I8_F16, _Float16, float>::type T;
+        typedef T vec __attribute__((ext_vector_type(C)));
+        T *o = static_cast<T *>(a.out) + at;
         if (whole) {
-            *reinterpret_cast<f32x4_t *>(o) = f32x4_t{v[0], v[1], v[2], v[3]};
+            vec p;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                p[i] = static_cast<T>(v[i]);
+            *reinterpret_cast<vec *>(o) = p;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < C; ++i)
                 if (n + i < a.N)
-                    o[i] = v[i];
+                    o[i] = static_cast<T>(v[i]);
         }
     }
-}
-
-// Sums of channels n .. n + 3 (n a multiple of 4, n < N) of token m -> output.
-// s0 and s1: the sums of the first and second weight.
-template <int OUT>
-__device__ __forceinline__ void int8_finish4(const Int8GemmArgs &a, int m, int n, const i32x4_t &s0,
-                                             const i32x4_t &s1)
-{
-    const float xs = a.xs[m];
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = min(n + i, a.N - 1);
-        const float y = int8_scaled(s0[i], xs, a.s0[c]);
-        if constexpr (int8_two_weights(OUT))
-            v[i] = int8_gated<OUT>(y, int8_scaled(s1[i], xs, a.s1[c]));
-        else
-            v[i] = a.bias ? int8_biased(y, a.bias[c]) : y;
-    }
-    int8_store4<OUT>(a, m, n, v);
 }
 
 }  // namespace ffn

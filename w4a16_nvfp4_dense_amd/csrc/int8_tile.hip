@@ -1,196 +1,765 @@
-// int8_tile.hip -- the int8 product for many tokens: tiles of tokens and
-// channels, both operands staged through LDS.
+// int8_tile.hip -- the int8 product on tiles of tokens and channels, both
+// operands staged through LDS, by one persistent workgroup for each compute
+// unit.
 //
-// Mathematics. As int8_skinny.hip; here the reduction of a tile stays in one
-// workgroup's accumulators.
+// Mathematics. out[m, n] = xs[m] s[n] sum_k x[m, k] w[n, k] with exact int32
+// sums, so a reduction may be cut anywhere and added in any order.
 //
-// What bounds it: the matrix instructions (2 M N K operations), and for
-// middling M the weight stream.
+// What bounds it: the weight stream for few tokens, the matrix instructions
+// (2 M N K operations) for many.
 //
 // Layout. A stage holds 128 columns of BM token rows and BN weight rows, 128
 // bytes a row, written by direct global -> LDS loads of 16 bytes a lane (eight
-// rows for each wave instruction). Piece s of row i holds columns
-// 16 (s ^ (i / 2 % 8)), chosen by the address each lane loads from, so the 16
-// lanes that read one column piece of 16 consecutive rows touch all 64 banks
-// once. STAGES stages form a ring: stage k + STAGES - 1 is loaded while stage
-// k is multiplied, one barrier for each stage.
+// rows, whole 128-byte lines, for each wave instruction). Piece s of row i
+// holds columns 16 (s ^ (i / 2 % 8)), chosen by the address each lane loads
+// from, so the 16 lanes that read one column piece of 16 consecutive rows
+// touch all 64 banks once. STAGES stages form a ring that runs on over the
+// workgroup's tiles; one barrier for each stage.
+//
+// Work split. The tiles' stages, in tile order, are units. Every workgroup
+// takes `whole` tiles and then an equal share of the units of the tiles that
+// are left, so a tile may be shared by neighbouring workgroups. A workgroup
+// walks its share downwards: the tile that its share ends in the middle of
+// comes first, and its sums go to the workspace, with a ready word; the tile
+// that its share begins in the middle of comes last, and there it adds the
+// lower workgroups' sums, by then long written, and stores the tile. A
+// workgroup only ever waits for lower ones, which were started before it and
+// wait for nothing themselves before they publish, so every wait ends.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "int8.h"
 #include "int8_device.h"
 #include "kernels.h"
 
+// Every piece of the kernel is inlined: a closure left in memory would put the
+// loop's state there.
+#define FFN_INLINE __attribute__((always_inline))
+
 namespace ffn {
 namespace {
 
-constexpr int kBk = 128;  // columns (bytes of a row) of a stage
+constexpr int kBk = 128;                 // columns (bytes of a row) of a stage
+constexpr int kPieces = kBk / 16;        // 16-byte pieces of a row and stage
+constexpr int kLoadRows = 64 / kPieces;  // rows of a direct load
 
-// Swizzle of row i's pieces.
+// Swizzle of row i's pieces: the 16 lanes that read one piece of 16 consecutive
+// rows touch all 64 banks once.
 __device__ __forceinline__ int piece_swizzle(int i)
 {
     return (i >> 1) & 7;
 }
 
-// BM tokens x BN weight rows, WM x WN waves. For two weights each wave's weight
-// rows are its channels of w0 followed by the same channels of w1.
-template <int BM, int BN, int WM, int WN, int STAGES, int OUT>
-__global__ __launch_bounds__(WM *WN * 64) void int8_tile_kernel(Int8GemmArgs a, int tiles_m, int tiles_n)
+// Division by a number that the host knows: n / d = n m >> (31 + s) for
+// n < 2^31, with s = ceil(log2 d) and m = ceil(2^(31 + s) / d). A few scalar
+// instructions instead of two dozen: a kernel this short is held up by
+// fetching its prologue's instructions.
+struct Divisor {
+    uint32_t d, m, s;
+    __device__ __forceinline__ uint32_t divide(uint32_t n) const
+    {
+        return static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> (31 + s));
+    }
+};
+
+Divisor divisor(uint32_t d)
+{
+    Divisor v{d, 0, 0};
+    while ((uint64_t{1} << v.s) < d)
+        ++v.s;
+    v.m = static_cast<uint32_t>(((uint64_t{1} << (31 + v.s)) + d - 1) / d);
+    return v;
+}
+
+constexpr int kXcds = 8;
+constexpr int kBand = 8;  // tiles of tokens that are walked together
+
+struct Split {
+    int tiles_m, tiles_n;
+    int whole;                  // whole tiles of every workgroup
+    int shared;                 // tiles split over the workgroups, after those
+    int sharers;                // workgroups that have a share of them, at most one for each unit
+    int least, more;            // units of a share
+    int stages;                 // stages of a tile
+    int place_step;             // of a round's places between an XCD's and the next one's, or 0
+    Divisor by_stages, by_band, by_rows, by_last_rows;  // tiles of a band; its tiles of tokens, and the last one's
+    unsigned long long tag;     // of this launch
+    int32_t *part;              // BM * BN sums for each sharer
+    unsigned long long *ready;  // a word for each sharer
+
+    // Workgroup b's place in a round of whole tiles: those of one XCD (b % 8)
+    // take neighbouring tiles, which share operands in its L2.
+    __device__ __forceinline__ int chunk(int b, int G) const
+    {
+        return place_step ? b % kXcds * place_step + b / kXcds : b;
+    }
+};
+
+// The units of workgroup b: its whole tiles, then units [share(b), share(b + 1))
+// of the shared tiles: `least` each, one more for the first `more` sharers.
+__device__ __forceinline__ int share(const Split &s, int b)
+{
+    b = min(b, s.sharers);
+    return b * s.least + min(b, s.more);
+}
+
+// The workgroup that has unit u of the shared tiles. (Divisions run on the
+// vector unit; the results go back to scalar registers.)
+__device__ __forceinline__ int owner(const Split &s, int u)
+{
+    const int cut = s.more * (s.least + 1);
+    const uint32_t n = u < cut ? u : u - cut, d = u < cut ? s.least + 1 : s.least;
+    return __builtin_amdgcn_readfirstlane(static_cast<int>(n / d)) + (u < cut ? 0 : s.more);
+}
+
+// A position in a workgroup's units: the whole tiles, then the shared ones
+// from the highest down, the stages of each upwards.
+struct Cursor {
+    int tile, k, k_end;  // stage k of a tile; the workgroup has it up to k_end
+    int round, u0, u;    // units [u0, u) of the share are still to come, the tile's among them
+
+    __device__ __forceinline__ void segment(const Split &s, int b, int G)
+    {
+        if (round < s.whole) {
+            tile = round * G + s.chunk(b, G);
+            k = 0;
+            k_end = s.stages;
+        } else {
+            const int t = s.by_stages.divide(u - 1);
+            tile = s.whole * G + t;
+            k = max(u0 - t * s.stages, 0);
+            k_end = u - t * s.stages;
+        }
+    }
+    __device__ __forceinline__ void start(const Split &s, int b, int G)
+    {
+        round = 0;
+        u0 = share(s, b);
+        u = share(s, b + 1);
+        segment(s, b, G);
+    }
+    // Past the `units` units of this tile; false if that was the last one.
+    __device__ __forceinline__ bool advance(const Split &s, int b, int G, int units)
+    {
+        if (round < s.whole)
+            ++round;
+        else
+            u -= units;
+        if (round >= s.whole && u <= u0)
+            return false;
+        segment(s, b, G);
+        return true;
+    }
+};
+
+// The matrix instruction on fragments of F tokens x F channels (F = 16: 64
+// columns at a time, F = 32: 32 columns). Lane l holds row l % F of either
+// operand and the 16 bytes at piece l / F of a step; group g of its results
+// is channel l % F of tokens 8 g + 4 (l / F) .. + 3.
+template <int F>
+struct Mfma;
+template <>
+struct Mfma<16> {
+    typedef i32x4_t acc_t;
+    static __device__ __forceinline__ void go(acc_t &c, const i32x4_t &x, const i32x4_t &w)
+    {
+        c = __builtin_amdgcn_mfma_i32_16x16x64_i8(x, w, c, 0, 0, 0);
+    }
+};
+template <>
+struct Mfma<32> {
+    typedef int acc_t __attribute__((ext_vector_type(16)));
+    static __device__ __forceinline__ void go(acc_t &c, const i32x4_t &x, const i32x4_t &w)
+    {
+        c = __builtin_amdgcn_mfma_i32_32x32x32_i8(x, w, c, 0, 0, 0);
+    }
+};
+// A direct load of 16 bytes a lane to LDS, lane l to byte `at` + 16 l. Written in
+// assembly because the compiler makes the next LDS read wait for every direct
+// load that it knows of; here the waits are those of the ring. It has no
+// output register, and the other waits stay right: the compiler's counts of
+// loads in flight are at most too low, so its waits are at most too long. The
+// wait states are those between a vector instruction's write of a scalar
+// register, or a write of m0, and this.
+template <bool NT>
+__device__ __forceinline__ void load_to_lds(const u32x4_t &rsrc, uint32_t at, int offset, int scalar_offset)
+{
+    const auto scalar = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(v)); };
+    const u32x4_t buffer = {scalar(rsrc[0]), scalar(rsrc[1]), scalar(rsrc[2]), scalar(rsrc[3])};
+    if constexpr (NT)
+        asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                     :
+                     : "v"(offset), "s"(buffer), "s"(scalar(scalar_offset)), "{m0}"(scalar(at))
+                     : "memory");
+    else
+        asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                     :
+                     : "v"(offset), "s"(buffer), "s"(scalar(scalar_offset)), "{m0}"(scalar(at))
+                     : "memory");
+}
+
+template <class A>
+__device__ __forceinline__ i32x4_t group_of(const A &c, int g)
+{
+    return i32x4_t{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
+}
+
+// BM tokens x BN weight rows, WM x WN waves, fragments of F x F. A wave has
+// FC fragments of channels; row c of fragment f is channel FC c + f of the
+// wave's, so that a lane ends with FC consecutive channels of a token and a
+// wave stores whole lines. For two weights each wave's rows are its channels of
+// w0 followed by the same channels of w1. NT: the weights are read
+// non-temporally.
+template <int BM, int BN, int WM, int WN, int F, int STAGES, bool NT, int OUT>
+__global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs a, Split sp)
 {
     constexpr bool TWO = int8_two_weights(OUT);
     constexpr int WAVES = WM * WN;
     constexpr int ROWS = BM + BN;
-    constexpr int LOADS = ROWS / 8 / WAVES;          // direct loads of a wave and stage
-    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // fragments of a wave
-    constexpr int WR = BN / WN;                      // weight rows of a wave
-    constexpr int WC = TWO ? WR / 2 : WR;            // channels of a wave
-    constexpr int BC = WC * WN;                      // channels of a tile
-    static_assert(ROWS % (8 * WAVES) == 0 && BM % 8 == 0, "whole loads");
+    constexpr int LOADS_ALL = ROWS / kLoadRows;          // direct loads of a stage
+    constexpr int LOADS = (LOADS_ALL + WAVES - 1) / WAVES;  // the most of one wave
+    constexpr int FULL = LOADS_ALL - (LOADS - 1) * WAVES;   // waves with LOADS; the others have one fewer
+    constexpr int FM = BM / WM / F, FN = BN / WN / F;    // fragments of a wave
+    constexpr int NG = F * F / 256;                      // groups of four results of a lane and fragment
+    constexpr int STEPS = kBk * F / 1024;                // steps of a stage
+    constexpr int WR = BN / WN;                          // weight rows of a wave
+    constexpr int WC = TWO ? WR / 2 : WR;                // channels of a wave
+    constexpr int BC = WC * WN;                          // channels of a tile
+    constexpr int FC = WC / F;                           // fragments of channels of a wave
+    constexpr int STAGE = ROWS * kBk;
+    static_assert(BM % kLoadRows == 0 && WR % kLoadRows == 0 && WC % F == 0, "whole loads and fragments");
     extern __shared__ int8_t lds[];  // [STAGES][ROWS][kBk], tokens first
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int r = lane & 15, q = lane >> 4;
+    __builtin_assume(wave >= 0 && wave < WAVES);
+    const int r = lane % F, q = lane / F;
     const int wm = wave / WN, wn = wave % WN;
     const int K = a.K;
-    const int tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
-    const int m0 = tm * BM, n0 = tn * BC;
+    const int G = gridDim.x, b = blockIdx.x;
+    const int whole_k = K / kBk;  // stages of whole 128 columns
 
-    // Lane l of a load covers piece l % 8 of row l / 8 of eight rows.
-    const int8_t *src[LOADS];
-    int col[LOADS];
+    // Load j of a wave covers rows (j * WAVES + wave) * kLoadRows .. of a stage, all
+    // of the tokens, of w0 or of w1; lane l has one piece of row l / kPieces of
+    // those. `off` is that piece's place in its matrix, from the first row of
+    // the tile being loaded; rows past the end repeat the last one. (The
+    // buffers' bounds check would stop a read past a matrix all the same.)
+    const int lrow = lane / kPieces;
+    const auto column = [&](int j) FFN_INLINE {
+        return ((lane % kPieces) ^ piece_swizzle((j * WAVES + wave) * kLoadRows + lrow)) * 16;
+    };
+    // Tiles are numbered in bands of kBand tiles of tokens, the tokens fastest:
+    // 32 neighbours (an XCD's share of a round) are at most 8 x 4 tiles.
+    const auto tile_at = [&](int tile, int &m, int &n) FFN_INLINE {
+        const int band = sp.by_band.divide(tile), in = tile - band * sp.by_band.d;
+        const bool last = (band + 1) * kBand > sp.tiles_m;
+        n = last ? sp.by_last_rows.divide(in) : sp.by_rows.divide(in);
+        m = band * kBand + in - n * (last ? sp.by_last_rows.d : sp.by_rows.d);
+    };
+    const auto rows_from = [&](const int8_t *m, int row, int rows) FFN_INLINE {
+        // base, stride 0, size (of a tile's rows at most), raw-buffer format (as raw_buffer)
+        const uint64_t base = reinterpret_cast<uintptr_t>(m) + static_cast<uint64_t>(row) * K;
+        return u32x4_t{static_cast<uint32_t>(base), static_cast<uint32_t>(base >> 32) & 0xFFFF,
+                       static_cast<uint32_t>(min(rows - row, 256) * K), 0x00020000};
+    };
+    u32x4_t from_x, from_w0, from_w1;
+    int off[LOADS];
+    const auto aim = [&](int tile) FFN_INLINE {
+        int m0, n0;
+        tile_at(tile, m0, n0);
+        m0 *= BM;
+        n0 *= BC;
+        from_x = rows_from(a.x, m0, a.M);
+        from_w0 = rows_from(a.w0, n0, a.N);
+        from_w1 = TWO ? rows_from(a.w1, n0, a.N) : from_w0;
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-        const int row = (wave * LOADS + j) * 8 + (lane >> 3);
-        col[j] = ((lane & 7) ^ piece_swizzle(row)) * 16;
-        if (row < BM) {
-            src[j] = a.x + static_cast<size_t>(min(m0 + row, a.M - 1)) * K + col[j];
-        } else {
-            const int i = row - BM, part = i / WR, in = i % WR;
-            const int n = min(n0 + part * WC + (TWO ? in % WC : in), a.N - 1);
-            src[j] = (TWO && in >= WC ? a.w1 : a.w0) + static_cast<size_t>(n) * K + col[j];
+        for (int j = 0; j < LOADS; ++j) {
+            const int row = (j * WAVES + wave) * kLoadRows + lrow;
+            const int i = row - BM, f = i % WR / F % FC;
+            const int from = i < 0 ? min(row, a.M - 1 - m0) : min(i / WR * WC + i % F * FC + f, a.N - 1 - n0);
+            off[j] = from * K + column(j);
         }
-    }
-    const int whole = K / kBk, stages = (K + kBk - 1) / kBk;
-
-    // Loads stage k into its ring slot: direct loads, or (a last stage of
-    // fewer columns) through registers with zeros past the end.
-    auto issue = [&](int k) {
-        int8_t *to = lds + (k % STAGES) * (ROWS * kBk);
-        if (k < whole) {
+    };
+    const auto source = [&](int j) FFN_INLINE {
+        const int i = (j * WAVES + wave) * kLoadRows - BM;
+        // (copies first: a choice between the variables would keep them in memory)
+        const u32x4_t x = from_x, w0 = from_w0, w1 = from_w1;
+        return i < 0 ? x : TWO && i % WR >= WC ? w1 : w0;
+    };
+    // Loads stage k into the ring at `to`. Of a last stage of fewer columns the
+    // pieces past the end get an offset past the buffer, which reads as zeros.
+    const auto issue = [&](int k, int to) FFN_INLINE {
+        const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((FFN_LDS int8_t *)lds)) + to;
+        const auto load = [&](int j, int offset) FFN_INLINE {
+            if (j == LOADS - 1 && wave >= FULL)
+                return;
+            const uint32_t rows = at + (j * WAVES + wave) * kLoadRows * kBk;
+            if (NT && (j * WAVES + wave) * kLoadRows >= BM)
+                load_to_lds<NT>(source(j), rows, offset, k * kBk);
+            else
+                load_to_lds<false>(source(j), rows, offset, k * kBk);
+        };
+        if (k < whole_k) {
 #pragma unroll
             for (int j = 0; j < LOADS; ++j)
-                __builtin_amdgcn_global_load_lds(reinterpret_cast<const void *>(src[j] + k * kBk),
-                                                 (FFN_LDS void *)(to + (wave * LOADS + j) * 8 * kBk), 16, 0, 0);
+                load(j, off[j]);
         } else {
 #pragma unroll
-            for (int j = 0; j < LOADS; ++j) {
-                i32x4_t v = {0, 0, 0, 0};
-                if (k * kBk + col[j] < K)
-                    v = *reinterpret_cast<const i32x4_t *>(src[j] + k * kBk);
-                *reinterpret_cast<i32x4_t *>(to + (wave * LOADS + j) * 8 * kBk + lane * 16) = v;
-            }
+            for (int j = 0; j < LOADS; ++j)
+                load(j, k * kBk + column(j) < K ? off[j] : INT_MIN);
         }
     };
 
-    i32x4_t acc[FN][FM];
+    typename Mfma<F>::acc_t acc[FN][FM];
+    const auto clear = [&]() FFN_INLINE {
 #pragma unroll
-    for (int f = 0; f < FN; ++f)
+        for (int f = 0; f < FN; ++f)
 #pragma unroll
-        for (int t = 0; t < FM; ++t)
-            acc[f][t] = i32x4_t{0, 0, 0, 0};
-
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        if (s < stages)
-            issue(s);
+            for (int t = 0; t < FM; ++t)
+                acc[f][t] = typename Mfma<F>::acc_t{};
+    };
 
     // row i, piece p of a stage at i * kBk + (p ^ swizzle(i)) * 16; the
     // swizzle of a fragment's row is that of r (fragments start at multiples
-    // of 16), and pieces 4 .. 7 are those of the second half with bit 2 set
+    // of 16), and a step's number is in the bits of p above q's
     const int frag = r * kBk + ((q ^ piece_swizzle(r)) * 16);
     const int xoff = wm * (BM / WM) * kBk + frag;
     const int woff = (BM + wn * WR) * kBk + frag;
-
-    for (int k = 0; k < stages; ++k) {
-        // stage k has landed once at most the later stages' loads are in flight
-        if (k + STAGES - 1 <= whole)
-            wait_vmcnt<(STAGES - 2) * LOADS>();
-        else
-            wait_vmcnt<0>();
-        lds_barrier();
-        if (k + STAGES - 1 < stages)
-            issue(k + STAGES - 1);
-        const int8_t *st = lds + (k % STAGES) * (ROWS * kBk);
+    typedef i32x4_t Weights[FN];
+    typedef i32x4_t Tokens[FM];
+    const auto read = [&](int st, int s, Weights &w, Tokens &x) FFN_INLINE {
+        const int flip = s * (1024 / F);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            i32x4_t w[FN], x[FM];
+        for (int f = 0; f < FN; ++f)
+            w[f] = *reinterpret_cast<const i32x4_t *>(lds + st + (woff ^ flip) + f * F * kBk);
 #pragma unroll
-            for (int f = 0; f < FN; ++f)
-                w[f] = *reinterpret_cast<const i32x4_t *>(st + (woff ^ (h * 64)) + f * 16 * kBk);
+        for (int t = 0; t < FM; ++t)
+            x[t] = *reinterpret_cast<const i32x4_t *>(lds + st + (xoff ^ flip) + t * F * kBk);
+    };
+    const auto products = [&](const Weights &w, const Tokens &x, int f0, int f1) FFN_INLINE {
+#pragma unroll
+        for (int f = f0; f < f1; ++f)
 #pragma unroll
             for (int t = 0; t < FM; ++t)
-                x[t] = *reinterpret_cast<const i32x4_t *>(st + (xoff ^ (h * 64)) + t * 16 * kBk);
-#pragma unroll
-            for (int f = 0; f < FN; ++f)
-#pragma unroll
-                for (int t = 0; t < FM; ++t)
-                    acc[f][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[f], x[t], acc[f][t], 0, 0, 0);
-        }
-    }
+                Mfma<F>::go(acc[f][t], x[t], w[f]);
+    };
 
-    constexpr int FC = WC / 16;  // fragments of channels
+    const auto slot_at = [&](int f, int t, int g) FFN_INLINE {
+        return (((wave * FN + f) * FM + t) * NG + g) * 1024 + lane * 16;
+    };
+    const auto slot_of = [&](int w) FFN_INLINE {
+        return raw_buffer(sp.part + static_cast<size_t>(w) * (BM * BN), BM * BN * 4);
+    };
+    // Tokens in a tile from this lane's first one on; the sums of others are not
+    // kept.
+    const auto tokens_of = [&](int tile) FFN_INLINE {
+        int m, n;
+        tile_at(tile, m, n);
+        return a.M - (m * BM + wm * (BM / WM) + 4 * q);
+    };
+    // This workgroup's sums of a tile that a higher workgroup finishes.
+    const auto publish = [&](int tile) FFN_INLINE {
+        const auto mine = slot_of(b);
+        const int tokens = tokens_of(tile);
 #pragma unroll
-    for (int f = 0; f < FC; ++f) {
-        const int n = n0 + wn * WC + 16 * f + 4 * q;
-        if (n >= a.N)
-            continue;
+        for (int t = 0; t < FM; ++t)
 #pragma unroll
-        for (int t = 0; t < FM; ++t) {
-            const int m = m0 + wm * (BM / WM) + 16 * t + r;
-            if (m < a.M)
-                int8_finish4<OUT>(a, m, n, acc[f][t], acc[TWO ? f + FC : f][t]);
+            for (int g = 0; g < NG; ++g)
+                if (F * t + 8 * g < tokens)
+#pragma unroll
+                    for (int f = 0; f < FN; ++f)
+                        store_device_coherent(mine, slot_at(f, t, g),
+                                              __builtin_bit_cast(f32x4_t, group_of(acc[f][t], g)));
+        wait_vmcnt<0>();
+        lds_barrier();
+        if (threadIdx.x == 0)
+            __hip_atomic_store(sp.ready + b, sp.tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    };
+    // Finishes a tile: outputs of this workgroup's sums plus those of the lower
+    // workgroups that share it, if any (`first` .. b - 1). Their loads come a
+    // few groups of a few slots at a time, 32 registers in flight.
+    const auto store = [&](int tile, int first) FFN_INLINE {
+        int m0, n;
+        tile_at(tile, m0, n);
+        m0 = m0 * BM + wm * (BM / WM) + 4 * q;
+        n = n * BC + wn * WC + FC * r;
+        const int tokens = a.M - m0;
+        constexpr int GROUPS = FM * NG;                          // of a fragment of channels
+        constexpr int ROOM = 8;                                  // groups in flight
+        constexpr int ONCE = FN >= ROOM ? 1 : (GROUPS < ROOM / FN ? GROUPS : ROOM / FN);
+        constexpr int SLOTS = ROOM / (FN * ONCE) > 0 ? ROOM / (FN * ONCE) : 1;
+        static_assert(GROUPS % ONCE == 0, "whole pieces");
+        float xs[ONCE][4], next_xs[ONCE][4], s0[FC], s1[FC], bias[FC];
+        const auto scales_of = [&](float(&to)[ONCE][4], int j0) FFN_INLINE {
+#pragma unroll
+            for (int j = 0; j < ONCE; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    to[j][e] = a.xs[min(m0 + F * ((j0 + j) / NG) + 8 * ((j0 + j) % NG) + e, a.M - 1)];
+        };
+        scales_of(next_xs, 0);
+#pragma unroll
+        for (int i = 0; i < FC; ++i) {
+            const int c = min(n + i, a.N - 1);
+            s0[i] = a.s0[c];
+            s1[i] = TWO ? a.s1[c] : 0.0f;
+            bias[i] = !TWO && a.bias ? a.bias[c] : 0.0f;
+        }
+        if (first < b)
+            wait_ready([&](int i) { return sp.ready + first + i; }, b - first, sp.tag);
+#pragma unroll
+        for (int j0 = 0; j0 < GROUPS; j0 += ONCE) {
+#pragma unroll
+            for (int j = 0; j < ONCE; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    xs[j][e] = next_xs[j][e];
+            if (j0 + ONCE < GROUPS)
+                scales_of(next_xs, j0 + ONCE);
+            i32x4_t sum[ONCE][FN];
+#pragma unroll
+            for (int j = 0; j < ONCE; ++j)
+#pragma unroll
+                for (int f = 0; f < FN; ++f)
+                    sum[j][f] = group_of(acc[f][(j0 + j) / NG], (j0 + j) % NG);
+            for (int w0 = first; w0 < b; w0 += SLOTS) {
+                i32x4_t v[SLOTS][ONCE][FN];
+#pragma unroll
+                for (int i = 0; i < SLOTS; ++i) {
+                    const auto theirs = slot_of(min(w0 + i, b - 1));
+#pragma unroll
+                    for (int j = 0; j < ONCE; ++j)
+#pragma unroll
+                        for (int f = 0; f < FN; ++f) {
+                            const int t = (j0 + j) / NG, g = (j0 + j) % NG;
+                            v[i][j][f] = w0 + i < b && F * t + 8 * g < tokens
+                                             ? __builtin_bit_cast(i32x4_t,
+                                                                  load_device_coherent(theirs, slot_at(f, t, g)))
+                                             : i32x4_t{0, 0, 0, 0};
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+                    for (int j = 0; j < ONCE; ++j)
+#pragma unroll
+                        for (int f = 0; f < FN; ++f)
+                            sum[j][f] += v[i][j][f];
+            }
+#pragma unroll
+            for (int j = 0; j < ONCE; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int at = F * ((j0 + j) / NG) + 8 * ((j0 + j) % NG) + e;  // token, from m0
+                    if (at >= tokens || n >= a.N)
+                        continue;
+                    float v[FC];
+#pragma unroll
+                    for (int f = 0; f < FC; ++f) {
+                        const float y = int8_scaled(sum[j][f][e], xs[j][e], s0[f]);
+                        if constexpr (TWO)
+                            v[f] = int8_gated<OUT>(y, int8_scaled(sum[j][f + FC][e], xs[j][e], s1[f]));
+                        else
+                            v[f] = a.bias ? int8_biased(y, bias[f]) : y;
+                    }
+                    int8_store<OUT, FC>(a, m0 + at, n, v);
+                }
+            __builtin_amdgcn_sched_barrier(0);  // (one piece's values at a time in registers)
+        }
+        if (first < b) {
+            // the words are cleared once every wave has seen them, so that a
+            // replay of this launch (the same tag) starts afresh
+            lds_barrier();
+            if (threadIdx.x < b - first)
+                __hip_atomic_store(sp.ready + first + threadIdx.x, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    };
+
+    // One read among the products of a step, again and again.
+    const auto interleave = [&]() FFN_INLINE {
+#pragma unroll
+        for (int i = 0; i < FN + FM; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, FN * FM / (FN + FM), 0);  // products
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                    // LDS read
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, FN * FM, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    const int total = sp.whole * sp.stages + share(sp, b + 1) - share(sp, b);
+    if (total == 0)
+        return;
+    Cursor ld, at;
+    ld.start(sp, b, G);
+    at = ld;
+    int to = 0;        // where in the ring the next unit is loaded
+    int st = 0;        // and where the unit to multiply is
+    int rest = total;  // units to load
+    int ld_units = ld.k_end - ld.k;
+    const auto load_next = [&]() FFN_INLINE {
+        issue(ld.k, to);
+        to = to + STAGE == STAGES * STAGE ? 0 : to + STAGE;
+        if (--rest > 0 && ++ld.k == ld.k_end) {
+            ld.advance(sp, b, G, ld_units);
+            ld_units = ld.k_end - ld.k;
+            aim(ld.tile);
+        }
+    };
+    aim(ld.tile);
+#pragma unroll 1
+    for (int s = 0; s < STAGES - 1 && rest > 0; ++s)
+        load_next();
+    int spare = total - (STAGES - 1);  // units past those the ring holds now
+    // To the next unit, every wave being done with the one before: it has
+    // landed once at most the STAGES - 2 later ones' loads are in flight (loads
+    // return in order; a last stage through registers has waited for
+    // everything before it). Its predecessor's slot takes the next load.
+    const auto enter = [&]() FFN_INLINE {
+        if (spare < 0)
+            wait_vmcnt<0>();
+        else if (FULL == WAVES || wave < FULL)
+            wait_vmcnt<(STAGES - 2) * LOADS>();
+        else
+            wait_vmcnt<(STAGES - 2) * (LOADS - 1)>();
+        lds_barrier();
+        if (spare > 0)
+            load_next();
+        --spare;
+    };
+    const auto leave = [&]() FFN_INLINE { st = st + STAGE == STAGES * STAGE ? 0 : st + STAGE; };
+    // After a tile's last unit; false after the workgroup's last.
+    const auto finish = [&]() FFN_INLINE {
+        if (at.k_end < sp.stages)
+            publish(at.tile);
+        else
+            store(at.tile, at.k > 0 ? owner(sp, (at.tile - sp.whole * G) * sp.stages) : b);
+        // nothing that the compiler knows to be in flight goes into the next
+        // tile's loop: its waits there would take the ring's loads along
+        wait_vmcnt<0>();
+        return at.advance(sp, b, G, at.k_end - at.k);
+    };
+    if constexpr (FN * FM * F * F / 64 < 128) {
+        // few fragments: all of a unit's are read, then all multiplied, so the
+        // read latency is met once a unit
+        do {
+            clear();
+            for (int n = at.k_end - at.k; n > 0; --n) {
+                enter();
+                Weights w[STEPS];
+                Tokens x[STEPS];
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s)
+                    read(st, s, w[s], x[s]);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s)
+                    products(w[s], x[s], 0, FN);
+                leave();
+            }
+        } while (finish());
+    } else {
+        // many: the next step's fragments are read while one step's are
+        // multiplied, over the units' bounds too
+        Weights w[2];
+        Tokens x[2];
+        enter();
+        read(st, 0, w[0], x[0]);
+        for (;;) {
+            clear();
+            for (int n = at.k_end - at.k; n > 1; --n) {
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    // (products on either side of the barrier keep the matrix
+                    // cores busy over it)
+                    const int before = s + 1 == STEPS ? FN / 2 : 0;
+                    if (s + 1 == STEPS) {
+                        products(w[s % 2], x[s % 2], 0, before);
+                        __builtin_amdgcn_sched_barrier(0);
+                        enter();
+                        leave();
+                    }
+                    read(st, (s + 1) % STEPS, w[(s + 1) % 2], x[(s + 1) % 2]);
+                    products(w[s % 2], x[s % 2], before, FN);
+                    interleave();
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                if (s + 1 < STEPS)
+                    read(st, s + 1, w[(s + 1) % 2], x[(s + 1) % 2]);
+                products(w[s % 2], x[s % 2], 0, FN);
+            }
+            if (!finish())
+                return;
+            enter();
+            leave();
+            read(st, 0, w[0], x[0]);
         }
     }
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, int OUT>
-hipError_t launch_t(const Int8GemmArgs &a, hipStream_t stream)
+constexpr size_t round256(size_t n)
+{
+    return (n + 255) & ~static_cast<size_t>(255);
+}
+
+// A launch: the tile shape's numbers and how its tiles are split.
+struct Plan {
+    int groups;  // workgroups
+    Split split;
+    size_t part_bytes, word_bytes;
+};
+
+template <int BM, int BN, int OUT>
+Plan plan(const Int8GemmArgs &a)
 {
     constexpr int channels = int8_two_weights(OUT) ? BN / 2 : BN;
-    auto kern = int8_tile_kernel<BM, BN, WM, WN, STAGES, OUT>;
+    Plan p{};
+    Split &s = p.split;
+    s.tiles_m = (a.M + BM - 1) / BM;
+    s.tiles_n = (a.N + channels - 1) / channels;
+    s.stages = (a.K + kBk - 1) / kBk;
+    const long tiles = static_cast<long>(s.tiles_m) * s.tiles_n;
+    const int cus = device_cu_count();
+    p.groups = static_cast<int>(std::min<long>(cus, std::max<long>(tiles, tiles * s.stages / 4)));
+    // With tiles left over after a single round, that round is shared out too,
+    // so that a share is at least a tile long and a tile has at most three
+    // parts. (After more rounds the left-over tiles alone are shared: 1-3%
+    // faster at 4 rounds and a quarter, where a round's sums exchanged are
+    // 64 MB.)
+    s.whole = static_cast<int>(tiles / p.groups);
+    if (s.whole == 1 && tiles % p.groups != 0)
+        s.whole = 0;
+    s.shared = static_cast<int>(tiles - static_cast<long>(s.whole) * p.groups);
+    // at least four units to a share
+    const long units = static_cast<long>(s.shared) * s.stages;
+    s.sharers = static_cast<int>(std::min<long>(p.groups, std::max<long>(1, units / 4)));
+    s.place_step = p.groups % kXcds == 0 ? p.groups / kXcds : 0;
+    s.by_stages = divisor(s.stages);
+    s.by_band = divisor(kBand * s.tiles_n);
+    s.by_rows = divisor(kBand);
+    s.by_last_rows = divisor(s.tiles_m % kBand ? s.tiles_m % kBand : kBand);
+    if (s.shared > 0) {
+        s.least = s.shared * s.stages / s.sharers;
+        s.more = s.shared * s.stages % s.sharers;
+        p.part_bytes = round256(static_cast<size_t>(s.sharers) * BM * BN * 4);
+        p.word_bytes = round256(static_cast<size_t>(s.sharers) * 8);
+    }
+    return p;
+}
+
+template <int BM, int BN, int WM, int WN, int F, int STAGES, bool NT, int OUT>
+hipError_t launch_t(const Int8GemmArgs &a, void *workspace, size_t *need, hipStream_t stream)
+{
+    Plan p = plan<BM, BN, OUT>(a);
+    if (need) {
+        *need = p.part_bytes + p.word_bytes;
+        return hipSuccess;
+    }
+    auto kern = int8_tile_kernel<BM, BN, WM, WN, F, STAGES, NT, OUT>;
     constexpr int lds = STAGES * (BM + BN) * kBk;
     static std::atomic<uint64_t> lds_done{0};
     hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), lds, lds_done);
     if (e != hipSuccess)
         return e;
-    const int tm = (a.M + BM - 1) / BM, tn = (a.N + channels - 1) / channels;
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(tm) * tn), dim3(WM * WN * 64), lds, stream, a, tm, tn);
+    if (p.split.shared > 0) {
+        p.split.tag = launch_tag();
+        p.split.part = static_cast<int32_t *>(workspace);
+        p.split.ready = reinterpret_cast<unsigned long long *>(static_cast<char *>(workspace) + p.part_bytes);
+    }
+    hipLaunchKernelGGL(kern, dim3(p.groups), dim3(WM * WN * 64), lds, stream, a, p.split);
     return hipGetLastError();
 }
 
+// Weights of this size are read non-temporally where every byte is read once:
+// with those of the layer before them they do not stay in the 256 MB
+// last-level cache anyway. (178 MB at M = 1: 34.7 us for 38.1 with other
+// weights in between, but 33.6 for 31.4 if the same ones are read again and
+// again; 89 MB: no difference.)
+constexpr size_t kStreamBytes = size_t{128} << 20;
+
+// The tile of a product, by the tokens and by how many tiles it makes (times
+// on one MI355X, K/N as given, G the dual of K = 5120 and N = 17408):
+//   M <= 16, 32     the smallest that hold the tokens, 128 weight rows
+//   M <= 64         64 x 128 (G, M = 64: 47.1 us; 64 x 64: 48.6), 64 x 64
+//                   where 128 channels at a time leave half the compute units
+//                   without a tile (17408/5120: 24.6 us for 26.7)
+//   M <= 128, and more tokens that fill tiles of 256 badly: 128 x 128 (G,
+//                   M = 128: 54.0 us; 128 x 64: 65.9), 128 x 64 by the same
+//                   rule (17408/5120: 31.5 us for 35.2; M = 300, 4112/4099:
+//                   22.2 for 23.8)
+//   more            256 x 256 from 0.6 tiles a compute unit on (5120/17408,
+//                   M = 4096: 373 us; 256 x 128: 401; 128 x 128: 528),
+//                   256 x 128 from half a tile a compute unit on (G, M = 256:
+//                   65.8 us; 128 x 128: 90.5)
 template <int OUT>
-hipError_t launch_out(const Int8GemmArgs &a, hipStream_t stream)
+hipError_t launch_out(const Int8GemmArgs &a, void *workspace, size_t *need, hipStream_t stream)
 {
-    return launch_t<128, 128, 2, 2, 2, OUT>(a, stream);
+    constexpr bool TWO = int8_two_weights(OUT);
+    const long cus = device_cu_count();
+    const auto tiles = [&](long bm, long bn) {
+        const long channels = TWO ? bn / 2 : bn;
+        return (a.M + bm - 1) / bm * ((a.N + channels - 1) / channels);
+    };
+    if (a.M <= 64) {
+        const bool nt = static_cast<size_t>(a.N) * a.K * (TWO ? 2 : 1) >= kStreamBytes;
+        if (a.M <= 16)
+            return nt ? launch_t<16, 128, 1, 4, 16, 8, true, OUT>(a, workspace, need, stream)
+                      : launch_t<16, 128, 1, 4, 16, 8, false, OUT>(a, workspace, need, stream);
+        if (a.M <= 32)
+            return nt ? launch_t<32, 128, 1, 4, 16, 7, true, OUT>(a, workspace, need, stream)
+                      : launch_t<32, 128, 1, 4, 16, 7, false, OUT>(a, workspace, need, stream);
+        if constexpr (!TWO)
+            if (2 * tiles(64, 128) < cus)
+                return launch_t<64, 64, 4, 2, 16, 8, false, OUT>(a, workspace, need, stream);
+        return nt ? launch_t<64, 128, 2, 4, 16, 6, true, OUT>(a, workspace, need, stream)
+                  : launch_t<64, 128, 2, 4, 16, 6, false, OUT>(a, workspace, need, stream);
+    }
+    const long padded = (a.M + 255) / 256 * 256, padded_128 = (a.M + 127) / 128 * 128;
+    if (a.M > 128 && 8 * padded <= 9 * padded_128) {
+        if (10 * tiles(256, 256) >= 6 * cus)
+            return launch_t<256, 256, 4, 2, 32, 2, false, OUT>(a, workspace, need, stream);
+        if (2 * tiles(256, 128) >= cus)
+            return launch_t<256, 128, 4, 2, 32, 3, false, OUT>(a, workspace, need, stream);
+    }
+    if constexpr (!TWO)
+        if (2 * tiles(128, 128) < cus)
+            return launch_t<128, 64, 4, 2, 16, 6, false, OUT>(a, workspace, need, stream);
+    return launch_t<128, 128, 2, 4, 16, 4, false, OUT>(a, workspace, need, stream);
+}
+
+hipError_t launch(const Int8GemmArgs &a, Int8Out out, void *workspace, size_t *need, hipStream_t stream)
+{
+    switch (out) {
+    case I8_BF16:
+        return launch_out<I8_BF16>(a, workspace, need, stream);
+    case I8_F16:
+        return launch_out<I8_F16>(a, workspace, need, stream);
+    case I8_F32:
+        return launch_out<I8_F32>(a, workspace, need, stream);
+    case I8_H_SILU:
+        return launch_out<I8_H_SILU>(a, workspace, need, stream);
+    default:
+        return launch_out<I8_H_GELU>(a, workspace, need, stream);
+    }
 }
 
 }  // namespace
 
-hipError_t launch_int8_tile(const Int8GemmArgs &a, Int8Out out, hipStream_t stream)
+hipError_t launch_int8_gemm(const Int8GemmArgs &a, Int8Out out, void *workspace, hipStream_t stream)
 {
-    switch (out) {
-    case I8_BF16:
-        return launch_out<I8_BF16>(a, stream);
-    case I8_F16:
-        return launch_out<I8_F16>(a, stream);
-    case I8_F32:
-        return launch_out<I8_F32>(a, stream);
-    case I8_H_SILU:
-        return launch_out<I8_H_SILU>(a, stream);
-    default:
-        return launch_out<I8_H_GELU>(a, stream);
-    }
+    return launch(a, out, workspace, nullptr, stream);
+}
+
+size_t int8_gemm_workspace(int M, int K, int N, Int8Out out)
+{
+    Int8GemmArgs a{};
+    a.M = M;
+    a.K = K;
+    a.N = N;
+    size_t need = 0;
+    return launch(a, out, nullptr, &need, nullptr) == hipSuccess ? need : 0;
 }
 
 }  // namespace ffn
