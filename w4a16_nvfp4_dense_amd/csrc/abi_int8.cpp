@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "int8.h"
+#include "kernels.h"
 
 namespace {
 
@@ -83,7 +84,7 @@ struct Workspace {
     size_t h, codes, scales, split, total;
 };
 
-Workspace layout(int M, int K, int N)
+Workspace layout(int M, int K, int N, int cus)
 {
     Workspace w;
     const size_t e = static_cast<size_t>(M) * static_cast<size_t>(N);
@@ -91,19 +92,20 @@ Workspace layout(int M, int K, int N)
     w.codes = round256(4 * e);
     w.scales = w.codes + round256(e);
     w.split = w.scales + round256(4 * static_cast<size_t>(M));
-    w.total = w.split + std::max(ffn::int8_gemm_workspace(M, K, N, ffn::I8_H_SILU),
-                                 ffn::int8_gemm_workspace(M, N, K, ffn::I8_BF16));
+    w.total = w.split + std::max(ffn::int8_gemm_workspace(M, K, N, ffn::I8_H_SILU, cus),
+                                 ffn::int8_gemm_workspace(M, N, K, ffn::I8_BF16, cus));
     return w;
 }
 
 // h = act(gate) * up in fp32, then its int8 rows.
 hipError_t dual(const int8_t *xq, const float *xs, int M, int K, int N, const ffn_int8_weight *gate,
-                const ffn_int8_weight *up, int act, int8_t *hq, float *hs, float *h, void *split,
-                hipStream_t stream)
+                const ffn_int8_weight *up, int act, int8_t *hq, float *hs, char *workspace, const Workspace &w,
+                int cus, hipStream_t stream)
 {
-    const ffn::Int8GemmArgs a{xq, xs, gate->codes, up->codes, gate->scales, up->scales, nullptr, h, M, K, N};
-    const hipError_t e =
-        ffn::launch_int8_gemm(a, act == FFN_NVFP4_ACT_SILU ? ffn::I8_H_SILU : ffn::I8_H_GELU, split, stream);
+    float *h = reinterpret_cast<float *>(workspace + w.h);
+    const ffn::Int8GemmArgs a{xq, xs, gate->codes, up->codes, gate->scales, up->scales, nullptr, h, M, K, N, cus};
+    const hipError_t e = ffn::launch_int8_gemm(a, act == FFN_NVFP4_ACT_SILU ? ffn::I8_H_SILU : ffn::I8_H_GELU,
+                                               workspace + w.split, stream);
     if (e != hipSuccess)
         return e;
     ffn::Int8RowsArgs r{};
@@ -189,7 +191,7 @@ size_t ffn_int8_gemm_workspace_bytes(int M, int K, int N)
 {
     if (M == 0 || check_gemm(M, K, N) != FFN_NVFP4_OK)
         return 0;
-    return ffn::int8_gemm_workspace(M, K, N, ffn::I8_BF16);
+    return ffn::int8_gemm_workspace(M, K, N, ffn::I8_BF16, ffn::device_cu_count());
 }
 
 int ffn_int8_gemm(const int8_t *xq, const float *xs, int M, int K, int N, const ffn_int8_weight *w,
@@ -203,14 +205,15 @@ int ffn_int8_gemm(const int8_t *xq, const float *xs, int M, int K, int N, const 
         return FFN_NVFP4_ERR_ACT;
     if (M == 0)
         return FFN_NVFP4_OK;
-    const size_t need = ffn_int8_gemm_workspace_bytes(M, K, N);
+    const int cus = ffn::device_cu_count();
+    const size_t need = ffn::int8_gemm_workspace(M, K, N, ffn::I8_BF16, cus);
     if (!xq || !xs || !out || (need > 0 && !workspace))
         return FFN_NVFP4_ERR_NULL;
     if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(bias, 4) || !aligned(out, 16) || !aligned(workspace, 16))
         return FFN_NVFP4_ERR_ALIGN;
     if (workspace_bytes < need)
         return FFN_NVFP4_ERR_WORKSPACE;
-    const ffn::Int8GemmArgs a{xq, xs, w->codes, nullptr, w->scales, nullptr, bias, out, M, K, N};
+    const ffn::Int8GemmArgs a{xq, xs, w->codes, nullptr, w->scales, nullptr, bias, out, M, K, N, cus};
     return launch_status(ffn::launch_int8_gemm(a, out_kind(out_dtype), workspace, stream));
 }
 
@@ -218,7 +221,7 @@ size_t ffn_int8_workspace_bytes(int M, int K, int N)
 {
     if (M == 0 || check_ffn(M, K, N) != FFN_NVFP4_OK)
         return 0;
-    return layout(M, K, N).total;
+    return layout(M, K, N, ffn::device_cu_count()).total;
 }
 
 int ffn_int8_dual_gemm(const int8_t *xq, const float *xs, int M, int K, int N, const ffn_int8_weight *gate,
@@ -236,11 +239,11 @@ int ffn_int8_dual_gemm(const int8_t *xq, const float *xs, int M, int K, int N, c
         return FFN_NVFP4_ERR_NULL;
     if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(hq, 16) || !aligned(hs, 4) || !aligned(workspace, 16))
         return FFN_NVFP4_ERR_ALIGN;
-    if (workspace_bytes < ffn_int8_workspace_bytes(M, K, N))
+    const int cus = ffn::device_cu_count();
+    const Workspace w = layout(M, K, N, cus);
+    if (workspace_bytes < w.total)
         return FFN_NVFP4_ERR_WORKSPACE;
-    char *ws = static_cast<char *>(workspace);
-    return launch_status(dual(xq, xs, M, K, N, gate, up, act, hq, hs, reinterpret_cast<float *>(ws),
-                              ws + layout(M, K, N).split, stream));
+    return launch_status(dual(xq, xs, M, K, N, gate, up, act, hq, hs, static_cast<char *>(workspace), w, cus, stream));
 }
 
 int ffn_int8_forward(const int8_t *xq, const float *xs, int M, int K, int N, const ffn_int8_weight *gate,
@@ -259,17 +262,17 @@ int ffn_int8_forward(const int8_t *xq, const float *xs, int M, int K, int N, con
         return FFN_NVFP4_ERR_NULL;
     if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(out, 16) || !aligned(workspace, 16))
         return FFN_NVFP4_ERR_ALIGN;
-    if (workspace_bytes < ffn_int8_workspace_bytes(M, K, N))
+    const int cus = ffn::device_cu_count();
+    const Workspace w = layout(M, K, N, cus);
+    if (workspace_bytes < w.total)
         return FFN_NVFP4_ERR_WORKSPACE;
-    const Workspace w = layout(M, K, N);
     char *ws = static_cast<char *>(workspace);
     int8_t *hq = reinterpret_cast<int8_t *>(ws + w.codes);
     float *hs = reinterpret_cast<float *>(ws + w.scales);
-    const hipError_t e = dual(xq, xs, M, K, N, gate, up, act, hq, hs, reinterpret_cast<float *>(ws + w.h),
-                              ws + w.split, stream);
+    const hipError_t e = dual(xq, xs, M, K, N, gate, up, act, hq, hs, ws, w, cus, stream);
     if (e != hipSuccess)
         return FFN_NVFP4_ERR_LAUNCH;
-    const ffn::Int8GemmArgs a{hq, hs, down->codes, nullptr, down->scales, nullptr, nullptr, out, M, N, K};
+    const ffn::Int8GemmArgs a{hq, hs, down->codes, nullptr, down->scales, nullptr, nullptr, out, M, N, K, cus};
     return launch_status(ffn::launch_int8_gemm(a, out_kind(out_dtype), ws + w.split, stream));
 }
 

@@ -41,6 +41,7 @@ struct Int8GemmArgs {
     const float *bias;          // [N] or null
     void *out;
     int M, K, N;
+    int cus;                    // compute units of the device (device_cu_count())
 };
 
 constexpr bool int8_two_weights(int out)
@@ -51,6 +52,6 @@ constexpr bool int8_two_weights(int out)
 // The product (int8_tile.hip). `workspace` holds int8_gemm_workspace(...) bytes
 // (any contents): what workgroups that share a tile exchange.
 hipError_t launch_int8_gemm(const Int8GemmArgs &a, Int8Out out, void *workspace, hipStream_t stream);
-size_t int8_gemm_workspace(int M, int K, int N, Int8Out out);
+size_t int8_gemm_workspace(int M, int K, int N, Int8Out out, int cus);
 
 }  // namespace ffn

@@ -376,35 +376,58 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
         if (threadIdx.x == 0)
             __hip_atomic_store(sp.ready + b, sp.tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     };
+    // The scales of a tile, for this lane's FC channels and GROUPS groups of
+    // four tokens. Small tiles read them when a tile begins, so that they are
+    // there when it ends; large ones, which have no registers to spare, a
+    // piece at a time when it ends.
+    constexpr int GROUPS = FM * NG;
+    constexpr bool DEEP = FN * FM * F * F / 64 >= 128;
+    float scale_x[GROUPS][4], scale_0[FC], scale_1[FC], add[FC];
+    const auto place = [&](int tile, int &m, int &n) FFN_INLINE {
+        tile_at(tile, m, n);
+        m = m * BM + wm * (BM / WM) + 4 * q;
+        n = n * BC + wn * WC + FC * r;
+    };
+    const auto channel_scales = [&](int n) FFN_INLINE {
+#pragma unroll
+        for (int i = 0; i < FC; ++i) {
+            const int c = min(n + i, a.N - 1);
+            scale_0[i] = a.s0[c];
+            scale_1[i] = TWO ? a.s1[c] : 0.0f;
+            add[i] = !TWO && a.bias ? a.bias[c] : 0.0f;
+        }
+    };
+    const auto token_scales = [&](int m, int j0, int count) FFN_INLINE {  // of groups j0 .., into place 0 on
+#pragma unroll
+        for (int j = 0; j < count; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                scale_x[j][e] = a.xs[min(m + F * ((j0 + j) / NG) + 8 * ((j0 + j) % NG) + e, a.M - 1)];
+    };
+    const auto begin = [&](int tile) FFN_INLINE {
+        clear();
+        if constexpr (!DEEP) {
+            int m, n;
+            place(tile, m, n);
+            channel_scales(n);
+            token_scales(m, 0, GROUPS);
+        }
+    };
     // Finishes a tile: outputs of this workgroup's sums plus those of the lower
     // workgroups that share it, if any (`first` .. b - 1). Their loads come a
     // few groups of a few slots at a time, 32 registers in flight.
     const auto store = [&](int tile, int first) FFN_INLINE {
         int m0, n;
-        tile_at(tile, m0, n);
-        m0 = m0 * BM + wm * (BM / WM) + 4 * q;
-        n = n * BC + wn * WC + FC * r;
+        place(tile, m0, n);
         const int tokens = a.M - m0;
-        constexpr int GROUPS = FM * NG;                          // of a fragment of channels
-        constexpr int ROOM = 8;                                  // groups in flight
+        constexpr int ROOM = 8;  // groups in flight
         constexpr int ONCE = FN >= ROOM ? 1 : (GROUPS < ROOM / FN ? GROUPS : ROOM / FN);
         constexpr int SLOTS = ROOM / (FN * ONCE) > 0 ? ROOM / (FN * ONCE) : 1;
         static_assert(GROUPS % ONCE == 0, "whole pieces");
-        float xs[ONCE][4], next_xs[ONCE][4], s0[FC], s1[FC], bias[FC];
-        const auto scales_of = [&](float(&to)[ONCE][4], int j0) FFN_INLINE {
-#pragma unroll
-            for (int j = 0; j < ONCE; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    to[j][e] = a.xs[min(m0 + F * ((j0 + j) / NG) + 8 * ((j0 + j) % NG) + e, a.M - 1)];
-        };
-        scales_of(next_xs, 0);
-#pragma unroll
-        for (int i = 0; i < FC; ++i) {
-            const int c = min(n + i, a.N - 1);
-            s0[i] = a.s0[c];
-            s1[i] = TWO ? a.s1[c] : 0.0f;
-            bias[i] = !TWO && a.bias ? a.bias[c] : 0.0f;
+        float xs[ONCE][4];
+        if constexpr (DEEP) {
+            channel_scales(n);
+            token_scales(m0, 0, ONCE);
         }
         if (first < b)
             wait_ready([&](int i) { return sp.ready + first + i; }, b - first, sp.tag);
@@ -414,9 +437,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
             for (int j = 0; j < ONCE; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    xs[j][e] = next_xs[j][e];
-            if (j0 + ONCE < GROUPS)
-                scales_of(next_xs, j0 + ONCE);
+                    xs[j][e] = scale_x[DEEP ? j : j0 + j][e];
+            if constexpr (DEEP)
+                if (j0 + ONCE < GROUPS)
+                    token_scales(m0, j0 + ONCE, ONCE);
             i32x4_t sum[ONCE][FN];
 #pragma unroll
             for (int j = 0; j < ONCE; ++j)
@@ -457,11 +481,11 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
                     float v[FC];
 #pragma unroll
                     for (int f = 0; f < FC; ++f) {
-                        const float y = int8_scaled(sum[j][f][e], xs[j][e], s0[f]);
+                        const float y = int8_scaled(sum[j][f][e], xs[j][e], scale_0[f]);
                         if constexpr (TWO)
-                            v[f] = int8_gated<OUT>(y, int8_scaled(sum[j][f + FC][e], xs[j][e], s1[f]));
+                            v[f] = int8_gated<OUT>(y, int8_scaled(sum[j][f + FC][e], xs[j][e], scale_1[f]));
                         else
-                            v[f] = a.bias ? int8_biased(y, bias[f]) : y;
+                            v[f] = a.bias ? int8_biased(y, add[f]) : y;
                     }
                     int8_store<OUT, FC>(a, m0 + at, n, v);
                 }
@@ -539,11 +563,11 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
         wait_vmcnt<0>();
         return at.advance(sp, b, G, at.k_end - at.k);
     };
-    if constexpr (FN * FM * F * F / 64 < 128) {
+    if constexpr (!DEEP) {
         // few fragments: all of a unit's are read, then all multiplied, so the
         // read latency is met once a unit
         do {
-            clear();
+            begin(at.tile);
             for (int n = at.k_end - at.k; n > 0; --n) {
                 enter();
                 Weights w[STEPS];
@@ -566,7 +590,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
         enter();
         read(st, 0, w[0], x[0]);
         for (;;) {
-            clear();
+            begin(at.tile);
             for (int n = at.k_end - at.k; n > 1; --n) {
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s) {
@@ -621,7 +645,7 @@ Plan plan(const Int8GemmArgs &a)
     s.tiles_n = (a.N + channels - 1) / channels;
     s.stages = (a.K + kBk - 1) / kBk;
     const long tiles = static_cast<long>(s.tiles_m) * s.tiles_n;
-    const int cus = device_cu_count();
+    const int cus = a.cus;
     p.groups = static_cast<int>(std::min<long>(cus, std::max<long>(tiles, tiles * s.stages / 4)));
     // With tiles left over after a single round, that round is shared out too,
     // so that a share is at least a tile long and a tile has at most three
@@ -632,9 +656,12 @@ Plan plan(const Int8GemmArgs &a)
     if (s.whole == 1 && tiles % p.groups != 0)
         s.whole = 0;
     s.shared = static_cast<int>(tiles - static_cast<long>(s.whole) * p.groups);
-    // at least four units to a share
+    // At least four units to a share; and after whole rounds two parts of a
+    // tile, whose sums are then exchanged once (5120/17408, M = 4096: 372 us;
+    // four parts 387-408).
     const long units = static_cast<long>(s.shared) * s.stages;
-    s.sharers = static_cast<int>(std::min<long>(p.groups, std::max<long>(1, units / 4)));
+    s.sharers = static_cast<int>(std::min<long>(s.whole > 0 ? std::min(p.groups, 2 * s.shared) : p.groups,
+                                                std::max<long>(1, units / 4)));
     s.place_step = p.groups % kXcds == 0 ? p.groups / kXcds : 0;
     s.by_stages = divisor(s.stages);
     s.by_band = divisor(kBand * s.tiles_n);
@@ -697,7 +724,7 @@ template <int OUT>
 hipError_t launch_out(const Int8GemmArgs &a, void *workspace, size_t *need, hipStream_t stream)
 {
     constexpr bool TWO = int8_two_weights(OUT);
-    const long cus = device_cu_count();
+    const long cus = a.cus;
     const auto tiles = [&](long bm, long bn) {
         const long channels = TWO ? bn / 2 : bn;
         return (a.M + bm - 1) / bm * ((a.N + channels - 1) / channels);
@@ -752,9 +779,10 @@ hipError_t launch_int8_gemm(const Int8GemmArgs &a, Int8Out out, void *workspace,
     return launch(a, out, workspace, nullptr, stream);
 }
 
-size_t int8_gemm_workspace(int M, int K, int N, Int8Out out)
+size_t int8_gemm_workspace(int M, int K, int N, Int8Out out, int cus)
 {
     Int8GemmArgs a{};
+    a.cus = cus;
     a.M = M;
     a.K = K;
     a.N = N;
