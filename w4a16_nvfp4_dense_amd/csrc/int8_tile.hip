@@ -708,7 +708,10 @@ constexpr size_t kStreamBytes = size_t{128} << 20;
 
 // The tile of a product, by the tokens and by how many tiles it makes (times
 // on one MI355X, K/N as given, G the dual of K = 5120 and N = 17408):
-//   M <= 16, 32     the smallest that hold the tokens, 128 weight rows
+//   M <= 16, 32     the smallest that hold the tokens, 128 weight rows; 64 rows
+//                   where 128 at a time leave half the compute units without a
+//                   tile (17408/5120: M = 1 20.8 us for 22.2, M = 32 22.0 for
+//                   23.9; 21504/5376: no difference)
 //   M <= 64         64 x 128 (G, M = 64: 47.1 us; 64 x 64: 48.6), 64 x 64
 //                   where 128 channels at a time leave half the compute units
 //                   without a tile (17408/5120: 24.6 us for 26.7)
@@ -731,6 +734,11 @@ hipError_t launch_out(const Int8GemmArgs &a, void *workspace, size_t *need, hipS
     };
     if (a.M <= 64) {
         const bool nt = static_cast<size_t>(a.N) * a.K * (TWO ? 2 : 1) >= kStreamBytes;
+        if (a.M <= 32 && !nt)
+            if constexpr (!TWO)
+                if (2 * tiles(32, 128) < cus)
+                    return a.M <= 16 ? launch_t<16, 64, 1, 4, 16, 10, false, OUT>(a, workspace, need, stream)
+                                     : launch_t<32, 64, 1, 4, 16, 12, false, OUT>(a, workspace, need, stream);
         if (a.M <= 16)
             return nt ? launch_t<16, 128, 1, 4, 16, 8, true, OUT>(a, workspace, need, stream)
                       : launch_t<16, 128, 1, 4, 16, 8, false, OUT>(a, workspace, need, stream);
