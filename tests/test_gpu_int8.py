@@ -407,6 +407,24 @@ def test_forward_rows_do_not_depend_on_the_batch(K, N, act):
         assert same_bits(out[0:M:9], one[:n]), M
 
 
+@pytest.mark.parametrize("K,N", [(16, 16), (256, 512), (272, 1040), (512, 24560), (512, 24576), (512, 24592),
+                                 (5120, 17408), (8192, 16384), (20480, 1024)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_forward_of_one_token_is_its_parts(K, N, out_dtype):
+    """One token's h is quantised inside the down product where it is short enough: the bits are those of the
+    two calls, whose quantisation is a launch of its own."""
+    xq, xs, gate, up, down = _config(2, K, N, 11)
+    for act in (ffn.ACT_SILU, ffn.ACT_GELU_TANH):
+        hq, hs = ffn.int8_dual_gemm(xq[:1], xs[:1], gate, up, act)
+        ref = ffn.int8_gemm(hq, hs, down, out_dtype=out_dtype)
+        assert same_bits(ffn.int8_forward(xq[:1], xs[:1], gate, up, down, act, out_dtype), ref)
+    # nothing but zeros, and a NaN
+    zero = ffn.int8_forward(torch.zeros_like(xq[:1]), xs[:1], gate, up, down, out_dtype=out_dtype)
+    assert bool((zero == 0).all())
+    nan = ffn.int8_forward(xq[:1], torch.full_like(xs[:1], float("nan")), gate, up, down, out_dtype=out_dtype)
+    assert bool(nan.isnan().all())
+
+
 def test_forward_decode_shape_against_64_bits():
     M, K, N = 4, 5120, 17408
     xq, xs, gate, up, down = _config(M, K, N, 1)

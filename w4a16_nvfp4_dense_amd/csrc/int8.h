@@ -33,9 +33,14 @@ enum Int8Out : int {
     I8_H_GELU = 4,
 };
 
+// The longest row that a product takes as reals (96 registers of a thread hold
+// its share, and its codes fit LDS behind every ring).
+constexpr int kInt8RowMost = 24576;
+
 struct Int8GemmArgs {
     const int8_t *x;            // [M, K]
     const float *xs;            // [M]
+    const float *row;           // or, for M = 1 and K <= kInt8RowMost and one weight, x as reals [K], 16-byte aligned
     const int8_t *w0, *w1;      // [N, K]; w1 null for one weight
     const float *s0, *s1;       // [N]
     const float *bias;          // [N] or null

@@ -23,6 +23,15 @@ __device__ __forceinline__ uint32_t magnitude_bits(float v)
     return __float_as_uint(v) & 0x7FFFFFFFu;
 }
 
+// The maximum over a wave's lanes.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1)
+        v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), o)));
+    return v;
+}
+
 // A row's scale and the factor of its codes, from the largest magnitude's
 // bits: s = amax / 127 and 1 / s, each correctly rounded; 0 and 0 where s
 // would be subnormal (1 / s could overflow); NaN and 0 for a row with an

@@ -85,14 +85,6 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
-{
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1)
-        v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), o)));
-    return v;
-}
-
 struct Rows {
     Int8RowsArgs a;
     const uint8_t *nv_codes, *nv_scales;

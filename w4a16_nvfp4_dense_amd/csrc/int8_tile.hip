@@ -25,6 +25,11 @@
 // lower workgroups' sums, by then long written, and stores the tile. A
 // workgroup only ever waits for lower ones, which were started before it and
 // wait for nothing themselves before they publish, so every wait ends.
+//
+// A single token's real row (`row`, what is between the two products of a
+// decoded token) is quantised by every workgroup for itself before its first
+// stage, into LDS: the same codes as a launch of their own would give, without
+// that launch.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -211,13 +216,15 @@ __device__ __forceinline__ i32x4_t group_of(const A &c, int g)
 // wave's, so that a lane ends with FC consecutive channels of a token and a
 // wave stores whole lines. For two weights each wave's rows are its channels of
 // w0 followed by the same channels of w1. NT: the weights are read
-// non-temporally.
-template <int BM, int BN, int WM, int WN, int F, int STAGES, bool NT, int OUT>
+// non-temporally. ROW: one token, given as its real row (a.row); the stages
+// hold weights only, and its codes lie behind the ring.
+template <int BM, int BN, int WM, int WN, int F, int STAGES, bool NT, int OUT, bool ROW>
 __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs a, Split sp)
 {
     constexpr bool TWO = int8_two_weights(OUT);
     constexpr int WAVES = WM * WN;
-    constexpr int ROWS = BM + BN;
+    constexpr int XR = ROW ? 0 : BM;                     // token rows of a stage
+    constexpr int ROWS = XR + BN;
     constexpr int LOADS_ALL = ROWS / kLoadRows;          // direct loads of a stage
     constexpr int LOADS = (LOADS_ALL + WAVES - 1) / WAVES;  // the most of one wave
     constexpr int FULL = LOADS_ALL - (LOADS - 1) * WAVES;   // waves with LOADS; the others have one fewer
@@ -229,7 +236,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
     constexpr int BC = WC * WN;                          // channels of a tile
     constexpr int FC = WC / F;                           // fragments of channels of a wave
     constexpr int STAGE = ROWS * kBk;
-    static_assert(BM % kLoadRows == 0 && WR % kLoadRows == 0 && WC % F == 0, "whole loads and fragments");
+    static_assert(XR % kLoadRows == 0 && WR % kLoadRows == 0 && WC % F == 0, "whole loads and fragments");
     extern __shared__ int8_t lds[];  // [STAGES][ROWS][kBk], tokens first
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -276,13 +283,13 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
             const int row = (j * WAVES + wave) * kLoadRows + lrow;
-            const int i = row - BM, f = i % WR / F % FC;
+            const int i = row - XR, f = i % WR / F % FC;
             const int from = i < 0 ? min(row, a.M - 1 - m0) : min(i / WR * WC + i % F * FC + f, a.N - 1 - n0);
             off[j] = from * K + column(j);
         }
     };
     const auto source = [&](int j) FFN_INLINE {
-        const int i = (j * WAVES + wave) * kLoadRows - BM;
+        const int i = (j * WAVES + wave) * kLoadRows - XR;
         // (copies first: a choice between the variables would keep them in memory)
         const u32x4_t x = from_x, w0 = from_w0, w1 = from_w1;
         return i < 0 ? x : TWO && i % WR >= WC ? w1 : w0;
@@ -295,7 +302,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
             if (j == LOADS - 1 && wave >= FULL)
                 return;
             const uint32_t rows = at + (j * WAVES + wave) * kLoadRows * kBk;
-            if (NT && (j * WAVES + wave) * kLoadRows >= BM)
+            if (NT && (j * WAVES + wave) * kLoadRows >= XR)
                 load_to_lds<NT>(source(j), rows, offset, k * kBk);
             else
                 load_to_lds<false>(source(j), rows, offset, k * kBk);
@@ -325,17 +332,19 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
     // of 16), and a step's number is in the bits of p above q's
     const int frag = r * kBk + ((q ^ piece_swizzle(r)) * 16);
     const int xoff = wm * (BM / WM) * kBk + frag;
-    const int woff = (BM + wn * WR) * kBk + frag;
+    const int woff = (XR + wn * WR) * kBk + frag;
     typedef i32x4_t Weights[FN];
     typedef i32x4_t Tokens[FM];
-    const auto read = [&](int st, int s, Weights &w, Tokens &x) FFN_INLINE {
+    const auto read = [&](int st, int k, int s, Weights &w, Tokens &x) FFN_INLINE {
         const int flip = s * (1024 / F);
 #pragma unroll
         for (int f = 0; f < FN; ++f)
             w[f] = *reinterpret_cast<const i32x4_t *>(lds + st + (woff ^ flip) + f * F * kBk);
 #pragma unroll
         for (int t = 0; t < FM; ++t)
-            x[t] = *reinterpret_cast<const i32x4_t *>(lds + st + (xoff ^ flip) + t * F * kBk);
+            x[t] = *reinterpret_cast<const i32x4_t *>(
+                ROW ? lds + STAGES * STAGE + k * kBk + (q + s * (64 / F)) * 16
+                    : lds + st + (xoff ^ flip) + t * F * kBk);
     };
     const auto products = [&](const Weights &w, const Tokens &x, int f0, int f1) FFN_INLINE {
 #pragma unroll
@@ -382,6 +391,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
     // piece at a time when it ends.
     constexpr int GROUPS = FM * NG;
     constexpr bool DEEP = FN * FM * F * F / 64 >= 128;
+    float row_scale = 0.0f;  // of ROW
     float scale_x[GROUPS][4], scale_0[FC], scale_1[FC], add[FC];
     const auto place = [&](int tile, int &m, int &n) FFN_INLINE {
         tile_at(tile, m, n);
@@ -402,7 +412,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
         for (int j = 0; j < count; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                scale_x[j][e] = a.xs[min(m + F * ((j0 + j) / NG) + 8 * ((j0 + j) % NG) + e, a.M - 1)];
+                scale_x[j][e] = ROW ? row_scale : a.xs[min(m + F * ((j0 + j) / NG) + 8 * ((j0 + j) % NG) + e, a.M - 1)];
     };
     const auto begin = [&](int tile) FFN_INLINE {
         clear();
@@ -530,10 +540,46 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
             aim(ld.tile);
         }
     };
+    constexpr int THREADS = WAVES * 64;
+    constexpr int CHUNKS = ROW ? kInt8RowMost / (4 * THREADS) : 1;  // of four elements of the row, for each thread
+    f32x4_t row[CHUNKS];
+    if constexpr (ROW) {
+        const auto reals = raw_buffer(a.row, K * 4);  // (past its end: zeros)
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+            row[c] = __builtin_bit_cast(
+                f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(reals, (c * THREADS + threadIdx.x) * 16, 0, 0));
+        wait_vmcnt<0>();  // (before the ring's first loads, which the next wait would include)
+    }
     aim(ld.tile);
 #pragma unroll 1
     for (int s = 0; s < STAGES - 1 && rest > 0; ++s)
         load_next();
+    if constexpr (ROW) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                most = max(most, magnitude_bits(row[c][i]));
+        most = wave_max(most);
+        const int codes = STAGES * STAGE, span = sp.stages * kBk;
+        uint32_t *wave_most = reinterpret_cast<uint32_t *>(lds + codes + span);
+        if (lane == 0)
+            wave_most[wave] = most;
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i)
+            most = max(most, wave_most[i]);
+        float inverse;
+        int8_scale(most, row_scale, inverse);
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)  // (zeros up to the last stage's end)
+            if (const int at = (c * THREADS + threadIdx.x) * 4; at < span)
+                *reinterpret_cast<uint32_t *>(lds + codes + at) =
+                    int8_pack4(row[c][0], row[c][1], row[c][2], row[c][3], inverse);
+        // (the first stage's barrier is also between these writes and their reads)
+    }
     int spare = total - (STAGES - 1);  // units past those the ring holds now
     // To the next unit, every wave being done with the one before: it has
     // landed once at most the STAGES - 2 later ones' loads are in flight (loads
@@ -574,7 +620,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
                 Tokens x[STEPS];
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s)
-                    read(st, s, w[s], x[s]);
+                    read(st, at.k_end - n, s, w[s], x[s]);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s)
@@ -583,12 +629,13 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
             }
         } while (finish());
     } else {
+        static_assert(!ROW, "a single row has small tiles");
         // many: the next step's fragments are read while one step's are
         // multiplied, over the units' bounds too
         Weights w[2];
         Tokens x[2];
         enter();
-        read(st, 0, w[0], x[0]);
+        read(st, 0, 0, w[0], x[0]);
         for (;;) {
             begin(at.tile);
             for (int n = at.k_end - at.k; n > 1; --n) {
@@ -603,7 +650,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
                         enter();
                         leave();
                     }
-                    read(st, (s + 1) % STEPS, w[(s + 1) % 2], x[(s + 1) % 2]);
+                    read(st, 0, (s + 1) % STEPS, w[(s + 1) % 2], x[(s + 1) % 2]);
                     products(w[s % 2], x[s % 2], before, FN);
                     interleave();
                 }
@@ -611,14 +658,14 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 if (s + 1 < STEPS)
-                    read(st, s + 1, w[(s + 1) % 2], x[(s + 1) % 2]);
+                    read(st, 0, s + 1, w[(s + 1) % 2], x[(s + 1) % 2]);
                 products(w[s % 2], x[s % 2], 0, FN);
             }
             if (!finish())
                 return;
             enter();
             leave();
-            read(st, 0, w[0], x[0]);
+            read(st, 0, 0, w[0], x[0]);
         }
     }
 }
@@ -676,7 +723,7 @@ Plan plan(const Int8GemmArgs &a)
     return p;
 }
 
-template <int BM, int BN, int WM, int WN, int F, int STAGES, bool NT, int OUT>
+template <int BM, int BN, int WM, int WN, int F, int STAGES, bool NT, int OUT, bool ROW = false>
 hipError_t launch_t(const Int8GemmArgs &a, void *workspace, size_t *need, hipStream_t stream)
 {
     Plan p = plan<BM, BN, OUT>(a);
@@ -684,10 +731,13 @@ hipError_t launch_t(const Int8GemmArgs &a, void *workspace, size_t *need, hipStr
         *need = p.part_bytes + p.word_bytes;
         return hipSuccess;
     }
-    auto kern = int8_tile_kernel<BM, BN, WM, WN, F, STAGES, NT, OUT>;
-    constexpr int lds = STAGES * (BM + BN) * kBk;
+    auto kern = int8_tile_kernel<BM, BN, WM, WN, F, STAGES, NT, OUT, ROW>;
+    // the ring, and a row's codes and each wave's maximum
+    constexpr int ring = STAGES * ((ROW ? 0 : BM) + BN) * kBk, most = ring + (ROW ? kInt8RowMost + WM * WN * 4 : 0);
+    static_assert(most <= 160 * 1024, "LDS of a compute unit");
+    const int lds = ROW ? ring + p.split.stages * kBk + WM * WN * 4 : ring;
     static std::atomic<uint64_t> lds_done{0};
-    hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), lds, lds_done);
+    hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), most, lds_done);
     if (e != hipSuccess)
         return e;
     if (p.split.shared > 0) {
@@ -734,6 +784,11 @@ hipError_t launch_out(const Int8GemmArgs &a, void *workspace, size_t *need, hipS
     };
     if (a.M <= 64) {
         const bool nt = static_cast<size_t>(a.N) * a.K * (TWO ? 2 : 1) >= kStreamBytes;
+        if constexpr (!TWO)
+            if (a.row)
+                return nt                         ? launch_t<16, 128, 1, 4, 16, 8, true, OUT, true>(a, workspace, need, stream)
+                       : 2 * tiles(16, 128) < cus ? launch_t<16, 64, 1, 4, 16, 10, false, OUT, true>(a, workspace, need, stream)
+                                                  : launch_t<16, 128, 1, 4, 16, 8, false, OUT, true>(a, workspace, need, stream);
         if (a.M <= 32 && !nt)
             if constexpr (!TWO)
                 if (2 * tiles(32, 128) < cus)
