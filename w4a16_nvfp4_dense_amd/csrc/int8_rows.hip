@@ -102,7 +102,10 @@ __global__ __launch_bounds__(kRowThreads) void int8_rows_kernel(Rows p)
     const int chunks = p.a.cols / kVec;
     const size_t base = static_cast<size_t>(row) * p.a.cols;
 
-    float v[C][kVec];
+    // the norm's weights are loaded with the row where registers allow it, so
+    // that the outputs do not wait for them
+    constexpr bool AHEAD = NORM && C <= 4;
+    float v[C][kVec], nw[AHEAD ? C : 1][kVec];
     float sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -126,6 +129,8 @@ __global__ __launch_bounds__(kRowThreads) void int8_rows_kernel(Rows p)
             } else {
                 load8<T>(p.a.x, at, v[c]);
             }
+            if constexpr (AHEAD)
+                load8<WT>(p.a.weight, static_cast<size_t>(ch) * kVec, nw[c]);
             if constexpr (NORM) {
                 if (p.a.residual) {
                     float r[kVec];
@@ -157,7 +162,12 @@ __global__ __launch_bounds__(kRowThreads) void int8_rows_kernel(Rows p)
                 if (p.a.sum_out)
                     store8<T>(p.a.sum_out, at, v[c]);
                 float w[kVec];
-                load8<WT>(p.a.weight, static_cast<size_t>(ch) * kVec, w);
+                if constexpr (AHEAD)
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i)
+                        w[i] = nw[c][i];
+                else
+                    load8<WT>(p.a.weight, static_cast<size_t>(ch) * kVec, w);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
                     v[c][i] = v[c][i] * rstd * (p.a.weight_offset + w[i]);
