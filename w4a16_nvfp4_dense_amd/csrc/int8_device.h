@@ -23,12 +23,19 @@ __device__ __forceinline__ uint32_t magnitude_bits(float v)
     return __float_as_uint(v) & 0x7FFFFFFFu;
 }
 
-// The maximum over a wave's lanes.
+// The maximum over a wave's lanes, valid in the last one (lane 63), by the
+// lane moves of segment_sum (masked lanes give 0, below everything).
 __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1)
-        v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), o)));
+    const auto other = [&](auto move) __attribute__((always_inline)) {
+        v = max(v, __float_as_uint(move(__uint_as_float(v))));
+    };
+    other([](float x) { return dpp_move<0xB1>(x); });
+    other([](float x) { return dpp_move<0x4E>(x); });
+    other([](float x) { return dpp_move<0x141>(x); });
+    other([](float x) { return dpp_move<0x140>(x); });
+    other([](float x) { return dpp_move<0x142, 0xA>(x); });
+    other([](float x) { return dpp_move<0x143, 0xC>(x); });
     return v;
 }
 

@@ -77,14 +77,6 @@ __device__ __forceinline__ void store8(void *p, size_t at, const float (&v)[kVec
     }
 }
 
-__device__ __forceinline__ float wave_sum(float v)
-{
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1)
-        v += __shfl_xor(v, o);
-    return v;
-}
-
 struct Rows {
     Int8RowsArgs a;
     const uint8_t *nv_codes, *nv_scales;
@@ -146,8 +138,8 @@ __global__ __launch_bounds__(kRowThreads) void int8_rows_kernel(Rows p)
         }
     }
     if constexpr (NORM) {
-        sum = wave_sum(sum);
-        if (lane == 0)
+        sum = segment_sum<64>(sum);
+        if (lane == 63)
             sh_sum[wave] = sum;
         __syncthreads();
         sum = 0.0f;
@@ -183,7 +175,7 @@ __global__ __launch_bounds__(kRowThreads) void int8_rows_kernel(Rows p)
         for (int i = 0; i < kVec; ++i)
             m = max(m, magnitude_bits(v[c][i]));
     m = wave_max(m);
-    if (lane == 0)
+    if (lane == 63)
         sh_max[wave] = m;
     __syncthreads();
     m = 0;
@@ -208,7 +200,8 @@ hipError_t launch_rows(const Rows &p, hipStream_t stream)
 {
     const int chunks = p.a.cols / kVec;
     // the fewest chunks per thread that 1024 threads cover the row with, at
-    // least 2 (32 bytes in flight per tensor)
+    // least 2 (32 bytes in flight per tensor: 8192 rows of 5120 with a norm
+    // 47.4 us; 57.3 with one, which is 0.1 faster for a single row)
     int c = 2;
     while (c * kRowThreads < chunks)
         c *= 2;

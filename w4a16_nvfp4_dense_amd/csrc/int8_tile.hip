@@ -565,7 +565,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
         most = wave_max(most);
         const int codes = STAGES * STAGE, span = sp.stages * kBk;
         uint32_t *wave_most = reinterpret_cast<uint32_t *>(lds + codes + span);
-        if (lane == 0)
+        if (lane == 63)
             wave_most[wave] = most;
         lds_barrier();
 #pragma unroll
