@@ -577,3 +577,41 @@ def test_graph_replays(M):
         torch.cuda.synchronize()
         for a, b in zip((codes, scales, total, out, prod), ref):
             assert same_bits(a, b), k
+
+
+# ----------------------------------------------------------- beyond 32 bits
+def test_weight_past_4_gib():
+    """65600 x 65536 codes: the channels at either end, exactly (sums of at most 65536 * 2^14 = 2^30)."""
+    K, N = 65536, 65600
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    ws = torch.rand(N, generator=g, device="cuda") / K
+    for M in (1, 3, 40):
+        xq = torch.randint(-128, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+        xs = torch.rand(M, generator=g, device="cuda")
+        out = ffn.int8_gemm(xq, xs, ffn.Int8DeviceWeight(w, ws), out_dtype=torch.float32)
+        for at in (slice(0, 64), slice(N - 64, N)):
+            sums = xq.double() @ w[at].double().t().contiguous()
+            assert same_bits(out[:, at].contiguous(), sums.float() * xs[:, None] * ws[None, at]), (M, at)
+
+
+def test_output_past_4_gib():
+    M, K, N = 65536, 32, 65600
+    g = torch.Generator(device="cuda").manual_seed(6)
+    w = ffn.Int8DeviceWeight(torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8),
+                             torch.rand(N, generator=g, device="cuda"))
+    xq = torch.randint(-128, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    xs = torch.rand(M, generator=g, device="cuda")
+    out = ffn.int8_gemm(xq, xs, w)
+    for m in (0, 32767, 32768, M - 1):
+        assert same_bits(out[m:m + 1], ffn.int8_gemm(xq[m:m + 1], xs[m:m + 1], w)), m
+
+
+def test_rows_past_4_gib():
+    rows, cols = 65600, 65536
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    codes, scales = ffn.int8_quantize(x)
+    for r in (0, 32767, 32768, rows - 1):
+        q, s = ffn.int8_quantize(x[r:r + 1].clone())
+        assert same_bits(codes[r:r + 1], q) and same_bits(scales[r:r + 1], s), r
