@@ -16,11 +16,13 @@
 //
 // What bounds it, measured on one MI355X: memory for many rows, and for few the
 // launch and the two reductions' latency.
-//   norm with residual, bf16, 8192 x 5120   47.4 us, 294 MB: 6.2 TB/s
-//   the same, 1 x 5120                       4.8 us
-//   bf16 rows, 17408 x 5120                 42.4 us, 267 MB: 6.3 TB/s
-//   fp32 rows, 2048 x 17408                 27.5 us, 178 MB: 6.5 TB/s (part of
-//                                           it from the last-level cache)
+//   norm with residual, bf16, 8192 x 5120   52.2 us, 294 MB: 5.6 TB/s (47.4
+//                                           where x was written just before)
+//   the same, 1 x 5120                       3.4 us
+//   norm with residual, fp32, 333 x 5376     7.9 us, 23 MB
+//   bf16 rows, 17408 x 5120                 44.7 us, 267 MB: 6.0 TB/s
+//   fp16 rows, 3 x 17408                     3.2 us
+//   fp32 rows, 2048 x 17408, just written   27.1 us, 178 MB: 6.6 TB/s
 //   NVFP4 rows, 17408 x 5120                44.6 us, 139 MB, two thirds of them
 //                                           written: 3.1 TB/s
 #include <hip/hip_runtime.h>
@@ -211,8 +213,9 @@ hipError_t launch_rows(const Rows &p, hipStream_t stream)
 {
     const int chunks = p.a.cols / kVec;
     // the fewest chunks per thread that 1024 threads cover the row with, at
-    // least 2 (32 bytes in flight per tensor: 8192 rows of 5120 with a norm
-    // 47.4 us; 57.3 with one, which is 0.1 faster for a single row)
+    // least 2 (32 bytes in flight per tensor: 8192 rows of 5120 with a norm,
+    // x just written, 47.4 us; 57.3 with one, which is 0.1 faster for a single
+    // row)
     int c = 2;
     while (c * kRowThreads < chunks)
         c *= 2;

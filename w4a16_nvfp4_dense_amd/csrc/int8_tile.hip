@@ -12,10 +12,12 @@
 // time, and LDS reads and writes take as many cycles as the products. Measured
 // on one MI355X, weights not in a cache at M <= 128 (K/N; "dual" with h):
 //   M = 1     dual 5120/17408  32.5 us, 178 MB: 5.5 TB/s
-//             17408/5120, h quantised here too  21.6 us, 89 MB: 4.1 TB/s
+//             17408/5120, h quantised here too  19.0 - 21.6 us, 89 MB: 4.1 -
+//             4.7 TB/s; 5120/17408 18.2 us
 //   M = 32    dual 5376/21504  46.7 us, 231 MB: 5.0 TB/s
 //             21504/5376       27.3 us, 116 MB: 4.3 TB/s
 //   M = 128   dual 5120/17408  54.0 us, 845 TOPS; 17408/5120 33.6 us
+//   M = 300   4112/4099 fp32   21.2 us, 478 TOPS
 //   M = 2048  dual 5120/17408  380 us, 1920 TOPS; 17408/5120 194 us, 1880 TOPS
 //   M = 4096  5120/17408       330 - 351 us, 2080 - 2210 TOPS (4 waves of
 //             128 x 128 instead of 8 of 64 x 128, which read LDS less: 359)
