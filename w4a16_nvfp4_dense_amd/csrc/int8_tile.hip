@@ -37,8 +37,9 @@
 // comes first, and its sums go to the workspace, with a ready word; the tile
 // that its share begins in the middle of comes last, and there it adds the
 // lower workgroups' sums, by then long written, and stores the tile. A
-// workgroup only ever waits for lower ones, which were started before it and
-// wait for nothing themselves before they publish, so every wait ends.
+// workgroup only ever waits for lower ones, and after it has published its own
+// sums. An XCD starts its workgroups in order, so the lowest one that has not
+// published is running or the next to start there: every wait ends.
 //
 // A single token's real row (`row`, what is between the two products of a
 // decoded token) is quantised by every workgroup for itself before its first
