@@ -539,6 +539,26 @@ def test_other_stream_and_caller_buffers():
         assert same_bits(o, ref)
 
 
+@pytest.mark.parametrize("M", [1, 32, 300])
+def test_two_streams_at_once(M):
+    """Forwards on two streams, each with its own workspace, beside each other on the card: shared tiles of both
+    are finished right."""
+    K, N = 5120, 17408
+    xq, xs, gate, up, down = _config(M, K, N, 21)
+    ref = ffn.int8_forward(xq, xs, gate, up, down)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [torch.empty(ffn.int8_workspace_bytes(M, K, N), dtype=torch.uint8, device="cuda") for _ in streams]
+    outs = [[torch.empty_like(ref) for _ in range(20)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, ws, out in zip(streams, spaces, outs):
+            ffn.int8_forward(xq, xs, gate, up, down, out=out[i], workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for out in outs:
+        for o in out:
+            assert same_bits(o, ref)
+
+
 @pytest.mark.parametrize("M", [1, 24, 80, 300])
 def test_graph_replays(M):
     """Captured norm, forward and product: every replay against the eager
