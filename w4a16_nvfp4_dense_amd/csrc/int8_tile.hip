@@ -30,16 +30,16 @@
 // touch all 64 banks once. STAGES stages form a ring that runs on over the
 // workgroup's tiles; one barrier for each stage.
 //
-// Work split. The tiles' stages, in tile order, are units. Every workgroup
-// takes `whole` tiles and then an equal share of the units of the tiles that
-// are left, so a tile may be shared by neighbouring workgroups. A workgroup
-// walks its share downwards: the tile that its share ends in the middle of
-// comes first, and its sums go to the workspace, with a ready word; the tile
-// that its share begins in the middle of comes last, and there it adds the
-// lower workgroups' sums, by then long written, and stores the tile. A
-// workgroup only ever waits for lower ones, and after it has published its own
-// sums. An XCD starts its workgroups in order, so the lowest one that has not
-// published is running or the next to start there: every wait ends.
+// Work split (int8_split.h). Every workgroup takes whole tiles and then an equal
+// share of the units of the tiles that are left, walked downwards: the tile that
+// its share ends in the middle of comes first, the one that its share begins in
+// the middle of last. A workgroup with a part of a tile writes its sums to the
+// workspace and counts itself in the tile's word; the one that finds the others
+// counted adds their sums and stores the tile. The tile's last workgroup, which
+// reaches it last in its walk, looks first, and keeps its sums to itself where
+// it is the one (most tiles of two parts). Nothing ever waits for another
+// workgroup, so launches beside each other cannot hold each other up, and
+// int32 sums give the same bits whoever adds them.
 //
 // A single token's real row (`row`, what is between the two products of a
 // decoded token) is quantised by every workgroup for itself before its first
@@ -47,11 +47,11 @@
 // that launch.
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
 #include <climits>
 
 #include "int8.h"
 #include "int8_device.h"
+#include "int8_split.h"
 #include "kernels.h"
 
 // Every piece of the kernel is inlined: a closure left in memory would put the
@@ -61,7 +61,6 @@
 namespace ffn {
 namespace {
 
-constexpr int kBk = 128;                 // columns (bytes of a row) of a stage
 constexpr int kPieces = kBk / 16;        // 16-byte pieces of a row and stage
 constexpr int kLoadRows = 64 / kPieces;  // rows of a direct load
 
@@ -72,105 +71,25 @@ __device__ __forceinline__ int piece_swizzle(int i)
     return (i >> 1) & 7;
 }
 
-// Division by a number that the host knows: n / d = n m >> (31 + s) for
-// n < 2^31, with s = ceil(log2 d) and m = ceil(2^(31 + s) / d). A few scalar
-// instructions instead of two dozen: a kernel this short is held up by
-// fetching its prologue's instructions.
-struct Divisor {
-    uint32_t d, m, s;
-    __device__ __forceinline__ uint32_t divide(uint32_t n) const
+// A word of the workspace that workgroups on any XCD count in.
+struct SharedWord {
+    unsigned long long *at;
+    __device__ __forceinline__ bool exchange(unsigned long long &seen, unsigned long long next) const
     {
-        return static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> (31 + s));
+        return __hip_atomic_compare_exchange_strong(at, &seen, next, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT);
     }
-};
-
-Divisor divisor(uint32_t d)
-{
-    Divisor v{d, 0, 0};
-    while ((uint64_t{1} << v.s) < d)
-        ++v.s;
-    v.m = static_cast<uint32_t>(((uint64_t{1} << (31 + v.s)) + d - 1) / d);
-    return v;
-}
-
-constexpr int kXcds = 8;
-constexpr int kBand = 8;  // tiles of tokens that are walked together
-
-struct Split {
-    int tiles_m, tiles_n;
-    int whole;                  // whole tiles of every workgroup
-    int shared;                 // tiles split over the workgroups, after those
-    int sharers;                // workgroups that have a share of them, at most one for each unit
-    int least, more;            // units of a share
-    int stages;                 // stages of a tile
-    int place_step;             // of a round's places between an XCD's and the next one's, or 0
-    Divisor by_stages, by_band, by_rows, by_last_rows;  // tiles of a band; its tiles of tokens, and the last one's
-    unsigned long long tag;     // of this launch
-    int32_t *part;              // BM * BN sums for each sharer
-    unsigned long long *ready;  // a word for each sharer
-
-    // Workgroup b's place in a round of whole tiles: those of one XCD (b % 8)
-    // take neighbouring tiles, which share operands in its L2.
-    __device__ __forceinline__ int chunk(int b, int G) const
+    __device__ __forceinline__ unsigned long long add_one() const
     {
-        return place_step ? b % kXcds * place_step + b / kXcds : b;
+        return __hip_atomic_fetch_add(at, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-};
-
-// The units of workgroup b: its whole tiles, then units [share(b), share(b + 1))
-// of the shared tiles: `least` each, one more for the first `more` sharers.
-__device__ __forceinline__ int share(const Split &s, int b)
-{
-    b = min(b, s.sharers);
-    return b * s.least + min(b, s.more);
-}
-
-// The workgroup that has unit u of the shared tiles. (Divisions run on the
-// vector unit; the results go back to scalar registers.)
-__device__ __forceinline__ int owner(const Split &s, int u)
-{
-    const int cut = s.more * (s.least + 1);
-    const uint32_t n = u < cut ? u : u - cut, d = u < cut ? s.least + 1 : s.least;
-    return __builtin_amdgcn_readfirstlane(static_cast<int>(n / d)) + (u < cut ? 0 : s.more);
-}
-
-// A position in a workgroup's units: the whole tiles, then the shared ones
-// from the highest down, the stages of each upwards.
-struct Cursor {
-    int tile, k, k_end;  // stage k of a tile; the workgroup has it up to k_end
-    int round, u0, u;    // units [u0, u) of the share are still to come, the tile's among them
-
-    __device__ __forceinline__ void segment(const Split &s, int b, int G)
+    __device__ __forceinline__ unsigned long long load() const
     {
-        if (round < s.whole) {
-            tile = round * G + s.chunk(b, G);
-            k = 0;
-            k_end = s.stages;
-        } else {
-            const int t = s.by_stages.divide(u - 1);
-            tile = s.whole * G + t;
-            k = max(u0 - t * s.stages, 0);
-            k_end = u - t * s.stages;
-        }
+        return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    __device__ __forceinline__ void start(const Split &s, int b, int G)
+    __device__ __forceinline__ void clear() const
     {
-        round = 0;
-        u0 = share(s, b);
-        u = share(s, b + 1);
-        segment(s, b, G);
-    }
-    // Past the `units` units of this tile; false if that was the last one.
-    __device__ __forceinline__ bool advance(const Split &s, int b, int G, int units)
-    {
-        if (round < s.whole)
-            ++round;
-        else
-            u -= units;
-        if (round >= s.whole && u <= u0)
-            return false;
-        segment(s, b, G);
-        return true;
+        __hip_atomic_store(at, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 };
 
@@ -372,8 +291,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
     const auto slot_at = [&](int f, int t, int g) FFN_INLINE {
         return (((wave * FN + f) * FM + t) * NG + g) * 1024 + lane * 16;
     };
-    const auto slot_of = [&](int w) FFN_INLINE {
-        return raw_buffer(sp.part + static_cast<size_t>(w) * (BM * BN), BM * BN * 4);
+    const auto slot_of = [&](int number) FFN_INLINE {
+        return raw_buffer(sp.part + static_cast<size_t>(number) * (BM * BN), BM * BN * 4);
     };
     // Tokens in a tile from this lane's first one on; the sums of others are not
     // kept.
@@ -382,9 +301,9 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
         tile_at(tile, m, n);
         return a.M - (m * BM + wm * (BM / WM) + 4 * q);
     };
-    // This workgroup's sums of a tile that a higher workgroup finishes.
-    const auto publish = [&](int tile) FFN_INLINE {
-        const auto mine = slot_of(b);
+    // This workgroup's sums of a tile that it shares, to its slot.
+    const auto publish = [&](int tile, int number) FFN_INLINE {
+        const auto mine = slot_of(number);
         const int tokens = tokens_of(tile);
 #pragma unroll
         for (int t = 0; t < FM; ++t)
@@ -396,9 +315,40 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
                         store_device_coherent(mine, slot_at(f, t, g),
                                               __builtin_bit_cast(f32x4_t, group_of(acc[f][t], g)));
         wait_vmcnt<0>();
-        lds_barrier();
+        lds_barrier();  // every wave's stores have completed
+    };
+    // What thread 0 says, to every thread. (16 bytes behind the ring and a
+    // row's codes; two uses have a barrier between them.)
+    const int note_at = STAGES * STAGE + (ROW ? sp.stages * kBk : 0);
+    const auto agree = [&](auto decide) FFN_INLINE {
+        int *note = reinterpret_cast<int *>(lds + note_at);
         if (threadIdx.x == 0)
-            __hip_atomic_store(sp.ready + b, sp.tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            *note = decide() ? 1 : 0;
+        lds_barrier();
+        return __builtin_amdgcn_readfirstlane(*note) != 0;
+    };
+    // Whether this workgroup, with its part of a tile that `in` share, finishes the
+    // tile: then the others' sums are in their slots.
+    const auto take = [&](int tile, const Sharers &in) FFN_INLINE {
+        const int parts = in.last - in.first + 1;
+        const SharedWord word{sp.words + (tile - sp.whole * G)};
+        unsigned long long seen = 0;
+        if (b == in.last)
+            if (agree([&]() FFN_INLINE {
+                    seen = word.load();
+                    const bool all = seen == sp.tag + (parts - 1);
+                    if (all)
+                        word.clear();
+                    return all;
+                }))
+                return true;
+        publish(tile, slot_number(sp, in, b));
+        return agree([&]() FFN_INLINE {
+            const bool all = count_part(word, sp.tag, seen) == parts;
+            if (all)
+                word.clear();
+            return all;
+        });
     };
     // The scales of a tile, for this lane's FC channels and GROUPS groups of
     // four tokens. Small tiles read them when a tile begins, so that they are
@@ -438,10 +388,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
             token_scales(m, 0, GROUPS);
         }
     };
-    // Finishes a tile: outputs of this workgroup's sums plus those of the lower
-    // workgroups that share it, if any (`first` .. b - 1). Their loads come a
-    // few groups of a few slots at a time, 32 registers in flight.
-    const auto store = [&](int tile, int first) FFN_INLINE {
+    // Finishes a tile: outputs of this workgroup's sums plus those of the
+    // `others` workgroups that share it with this one. Their loads come a few
+    // groups of a few slots at a time, 32 registers in flight.
+    const auto store = [&](int tile, const Sharers &in, int others) FFN_INLINE {
         int m0, n;
         place(tile, m0, n);
         const int tokens = a.M - m0;
@@ -454,8 +404,6 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
             channel_scales(n);
             token_scales(m0, 0, ONCE);
         }
-        if (first < b)
-            wait_ready([&](int i) { return sp.ready + first + i; }, b - first, sp.tag);
 #pragma unroll
         for (int j0 = 0; j0 < GROUPS; j0 += ONCE) {
 #pragma unroll
@@ -472,17 +420,17 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
 #pragma unroll
                 for (int f = 0; f < FN; ++f)
                     sum[j][f] = group_of(acc[f][(j0 + j) / NG], (j0 + j) % NG);
-            for (int w0 = first; w0 < b; w0 += SLOTS) {
+            for (int w0 = 0; w0 < others; w0 += SLOTS) {
                 i32x4_t v[SLOTS][ONCE][FN];
 #pragma unroll
                 for (int i = 0; i < SLOTS; ++i) {
-                    const auto theirs = slot_of(min(w0 + i, b - 1));
+                    const auto theirs = slot_of(slot_number(sp, in, other_sharer(in, b, min(w0 + i, others - 1))));
 #pragma unroll
                     for (int j = 0; j < ONCE; ++j)
 #pragma unroll
                         for (int f = 0; f < FN; ++f) {
                             const int t = (j0 + j) / NG, g = (j0 + j) % NG;
-                            v[i][j][f] = w0 + i < b && F * t + 8 * g < tokens
+                            v[i][j][f] = w0 + i < others && F * t + 8 * g < tokens
                                              ? __builtin_bit_cast(i32x4_t,
                                                                   load_device_coherent(theirs, slot_at(f, t, g)))
                                              : i32x4_t{0, 0, 0, 0};
@@ -515,13 +463,6 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
                     int8_store<OUT, FC>(a, m0 + at, n, v);
                 }
             __builtin_amdgcn_sched_barrier(0);  // (one piece's values at a time in registers)
-        }
-        if (first < b) {
-            // the words are cleared once every wave has seen them, so that a
-            // replay of this launch (the same tag) starts afresh
-            lds_barrier();
-            if (threadIdx.x < b - first)
-                __hip_atomic_store(sp.ready + first + threadIdx.x, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
     };
 
@@ -579,7 +520,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
                 most = max(most, magnitude_bits(row[c][i]));
         most = wave_max(most);
         const int codes = STAGES * STAGE, span = sp.stages * kBk;
-        uint32_t *wave_most = reinterpret_cast<uint32_t *>(lds + codes + span);
+        uint32_t *wave_most = reinterpret_cast<uint32_t *>(lds + note_at);
         if (lane == 63)
             wave_most[wave] = most;
         lds_barrier();
@@ -615,10 +556,15 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
     const auto leave = [&]() FFN_INLINE { st = st + STAGE == STAGES * STAGE ? 0 : st + STAGE; };
     // After a tile's last unit; false after the workgroup's last.
     const auto finish = [&]() FFN_INLINE {
-        if (at.k_end < sp.stages)
-            publish(at.tile);
-        else
-            store(at.tile, at.k > 0 ? owner(sp, (at.tile - sp.whole * G) * sp.stages) : b);
+        Sharers in{b, b};
+        if (at.k > 0 || at.k_end < sp.stages) {
+            in = sharers_of(sp, at.tile - sp.whole * G);
+            // (divisions run on the vector unit; back to scalar registers)
+            in.first = __builtin_amdgcn_readfirstlane(in.first);
+            in.last = __builtin_amdgcn_readfirstlane(in.last);
+        }
+        if (in.first == in.last || take(at.tile, in))
+            store(at.tile, in, in.last - in.first);
         // nothing that the compiler knows to be in flight goes into the next
         // tile's loop: its waits there would take the ring's loads along
         wait_vmcnt<0>();
@@ -685,80 +631,29 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
     }
 }
 
-constexpr size_t round256(size_t n)
-{
-    return (n + 255) & ~static_cast<size_t>(255);
-}
-
-// A launch: the tile shape's numbers and how its tiles are split.
-struct Plan {
-    int groups;  // workgroups
-    Split split;
-    size_t part_bytes, word_bytes;
-};
-
-template <int BM, int BN, int OUT>
-Plan plan(const Int8GemmArgs &a)
-{
-    constexpr int channels = int8_two_weights(OUT) ? BN / 2 : BN;
-    Plan p{};
-    Split &s = p.split;
-    s.tiles_m = (a.M + BM - 1) / BM;
-    s.tiles_n = (a.N + channels - 1) / channels;
-    s.stages = (a.K + kBk - 1) / kBk;
-    const long tiles = static_cast<long>(s.tiles_m) * s.tiles_n;
-    const int cus = a.cus;
-    p.groups = static_cast<int>(std::min<long>(cus, std::max<long>(tiles, tiles * s.stages / 4)));
-    // With tiles left over after a single round, that round is shared out too,
-    // so that a share is at least a tile long and a tile has at most three
-    // parts. (After more rounds the left-over tiles alone are shared: 1-3%
-    // faster at 4 rounds and a quarter, where a round's sums exchanged are
-    // 64 MB.)
-    s.whole = static_cast<int>(tiles / p.groups);
-    if (s.whole == 1 && tiles % p.groups != 0)
-        s.whole = 0;
-    s.shared = static_cast<int>(tiles - static_cast<long>(s.whole) * p.groups);
-    // At least four units to a share; and after whole rounds two parts of a
-    // tile, whose sums are then exchanged once (5120/17408, M = 4096: 372 us;
-    // four parts 387-408).
-    const long units = static_cast<long>(s.shared) * s.stages;
-    s.sharers = static_cast<int>(std::min<long>(s.whole > 0 ? std::min(p.groups, 2 * s.shared) : p.groups,
-                                                std::max<long>(1, units / 4)));
-    s.place_step = p.groups % kXcds == 0 ? p.groups / kXcds : 0;
-    s.by_stages = divisor(s.stages);
-    s.by_band = divisor(kBand * s.tiles_n);
-    s.by_rows = divisor(kBand);
-    s.by_last_rows = divisor(s.tiles_m % kBand ? s.tiles_m % kBand : kBand);
-    if (s.shared > 0) {
-        s.least = s.shared * s.stages / s.sharers;
-        s.more = s.shared * s.stages % s.sharers;
-        p.part_bytes = round256(static_cast<size_t>(s.sharers) * BM * BN * 4);
-        p.word_bytes = round256(static_cast<size_t>(s.sharers) * 8);
-    }
-    return p;
-}
-
 template <int BM, int BN, int WM, int WN, int F, int STAGES, bool NT, int OUT, bool ROW = false>
 hipError_t launch_t(const Int8GemmArgs &a, void *workspace, size_t *need, hipStream_t stream)
 {
-    Plan p = plan<BM, BN, OUT>(a);
+    Plan p = int8_plan(a.M, a.K, a.N, BM, BN, int8_two_weights(OUT) ? BN / 2 : BN, a.cus);
     if (need) {
         *need = p.part_bytes + p.word_bytes;
         return hipSuccess;
     }
     auto kern = int8_tile_kernel<BM, BN, WM, WN, F, STAGES, NT, OUT, ROW>;
-    // the ring, and a row's codes and each wave's maximum
-    constexpr int ring = STAGES * ((ROW ? 0 : BM) + BN) * kBk, most = ring + (ROW ? kInt8RowMost + WM * WN * 4 : 0);
+    // the ring, a row's codes, and 16 bytes for what the waves tell each other (a
+    // row's maximum of each wave, then whether a tile is finished here)
+    constexpr int ring = STAGES * ((ROW ? 0 : BM) + BN) * kBk, most = ring + (ROW ? kInt8RowMost : 0) + 16;
     static_assert(most <= 160 * 1024, "LDS of a compute unit");
-    const int lds = ROW ? ring + p.split.stages * kBk + WM * WN * 4 : ring;
+    static_assert(!ROW || WM * WN <= 4, "a maximum of each wave");
+    const int lds = ring + (ROW ? p.split.stages * kBk : 0) + 16;
     static std::atomic<uint64_t> lds_done{0};
     hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), most, lds_done);
     if (e != hipSuccess)
         return e;
     if (p.split.shared > 0) {
-        p.split.tag = launch_tag();
+        p.split.tag = tag_of_launch(launch_tag());
         p.split.part = static_cast<int32_t *>(workspace);
-        p.split.ready = reinterpret_cast<unsigned long long *>(static_cast<char *>(workspace) + p.part_bytes);
+        p.split.words = reinterpret_cast<unsigned long long *>(static_cast<char *>(workspace) + p.part_bytes);
     }
     hipLaunchKernelGGL(kern, dim3(p.groups), dim3(WM * WN * 64), lds, stream, a, p.split);
     return hipGetLastError();
