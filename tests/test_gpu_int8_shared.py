@@ -1,5 +1,5 @@
-"""Int8 products whose tiles are shared by several workgroups, where calls run beside each other (needs an MI355X).
-The sums are exact, so everything is compared bit for bit."""
+"""Int8 products whose tiles are shared by several workgroups, where calls run beside each other and where a recorded
+call is replayed again and again (needs an MI355X). The sums are exact, so everything is compared bit for bit."""
 import pytest
 import torch
 
@@ -38,3 +38,33 @@ def test_many_streams_at_once(M, K, N):
     torch.cuda.synchronize()
     for o, p in (x for row in outs for x in row):
         assert same_bits(o, ref) and same_bits(p, prod)
+
+
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_replays_without_anything_between(M, K, N):
+    """A recorded forward and product, replayed for one input after another with nothing but the replays writing the
+    workspaces: what one replay leaves there must not pass for the next one's sums."""
+    _needs_sharing(M, K, N)
+    xq, xs, gate, up, down = _config(M, K, N, M + K)
+    inputs = [(xq.roll(31 * i, 1).contiguous(), (xs * (1 + i)).contiguous()) for i in range(5)]
+    refs = [(ffn.int8_forward(q, s, gate, up, down), ffn.int8_gemm(q, s, gate)) for q, s in inputs]
+    q, s = inputs[0][0].clone(), inputs[0][1].clone()
+    ws = torch.full((ffn.int8_workspace_bytes(M, K, N),), 0xFF, dtype=torch.uint8, device="cuda")
+    gws = torch.full((max(16, ffn.int8_gemm_workspace_bytes(M, K, N)),), 0xFF, dtype=torch.uint8, device="cuda")
+    out, prod = torch.empty_like(refs[0][0]), torch.empty_like(refs[0][1])
+
+    def step():
+        ffn.int8_forward(q, s, gate, up, down, out=out, workspace=ws)
+        ffn.int8_gemm(q, s, gate, out=prod, workspace=gws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in (0, 1, 2, 3, 4, 1, 0, 3):
+        q.copy_(inputs[i][0])
+        s.copy_(inputs[i][1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same_bits(out, refs[i][0]) and same_bits(prod, refs[i][1]), i
