@@ -75,8 +75,9 @@ typedef struct ffn_int8_weight {
  *   y[m, k] = t[m, k] / sqrt(mean_k t[m, k]^2 + eps) * (weight_offset + weight[k])
  *   sum_out = t, y_out = y, each rounded once to `dtype`;
  *   codes, scales = the int8 rows of y (of the unrounded y).
- * The norm is taken of t before it is rounded. mean t^2 is held in fp32: |t|
- * up to about 1e19 / sqrt(K) keeps it finite.
+ * The norm is taken of t before it is rounded. Every row of finite t has its
+ * norm: one whose squares do not fit fp32 is scaled by a power of two first. A
+ * row with an infinity or a NaN in t has s = NaN and codes 0.
  *   x          device [M, K] of `dtype`
  *   residual   device [M, K] of `dtype`, or NULL (t = x)
  *   weight     device [K] of `weight_dtype`, 16-byte aligned

@@ -3,7 +3,8 @@
 // the FFN), as they are (activations without a norm, weights at load), or
 // from an NVFP4 weight.
 //
-// Mathematics. t = x + r in fp32; y = t / sqrt(mean t^2 + eps) * (off + w);
+// Mathematics. t = x + r in fp32; y = t / sqrt(mean t^2 + eps) * (off + w), of
+// a row scaled by a power of two where the squares leave fp32's range;
 // s = max |y| / 127; q = rint(y * (1 / s)). The row's sum of squares and its
 // maximum need the whole row before its first output, so a row is held in
 // registers between them: one pass over memory, each element read once and
@@ -90,6 +91,21 @@ __device__ __forceinline__ void store8(void *p, size_t at, const float (&v)[kVec
     }
 }
 
+// The norm's mean square in fp32. From kLeastSquare on, squares too small for
+// fp32 (below 2^-126) are under 2^-30 of the mean. Where it is smaller, or not
+// finite, the row is scaled first, by the power of two that brings its largest
+// magnitude, or eps's root if that is larger, to [1, 4): the squares then sum to
+// between 1 and 16 cols, and t factor / sqrt(mean (t factor)^2 + eps factor^2)
+// is the same norm. (2^126 at most: a row of subnormals stays below 1, its
+// squares above 2^-46.)
+constexpr float kLeastSquare = 0x1p-96f;
+
+__device__ __forceinline__ float norm_factor(float most)
+{
+    const int exponent = static_cast<int>(__float_as_uint(most) >> 23);  // of a finite value: 0 .. 254
+    return __uint_as_float(static_cast<uint32_t>(254 - min(max(exponent, 1), 253)) << 23);
+}
+
 struct Rows {
     Int8RowsArgs a;
     const uint8_t *nv_codes, *nv_scales;
@@ -158,7 +174,42 @@ __global__ __launch_bounds__(kRowThreads) void int8_rows_kernel(Rows p)
         sum = 0.0f;
         for (int w = 0; w < waves; ++w)
             sum += sh_sum[w];
-        const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.a.cols) + p.a.eps);
+        const float cols = static_cast<float>(p.a.cols);
+        float square = sum / cols + p.a.eps, factor = 1.0f;
+        if (!(square >= kLeastSquare && square < __builtin_inff())) {
+            // (the same for every thread of the row)
+            uint32_t most = 0;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+                    most = max(most, magnitude_bits(v[c][i]));
+            most = wave_max(most);
+            if (lane == 63)
+                sh_max[wave] = most;
+            __syncthreads();
+            for (int w = 0; w < waves; ++w)
+                most = w == 0 ? sh_max[0] : max(most, sh_max[w]);
+            if (most > 0 && most < 0x7F800000u) {
+                factor = norm_factor(fmaxf(__uint_as_float(most), sqrtf(p.a.eps)));
+                sum = 0.0f;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i)
+                        sum += (v[c][i] * factor) * (v[c][i] * factor);
+                sum = segment_sum<64>(sum);
+                if (lane == 63)
+                    sh_sum[wave] = sum;
+                __syncthreads();
+                sum = 0.0f;
+                for (int w = 0; w < waves; ++w)
+                    sum += sh_sum[w];
+                square = sum / cols + p.a.eps * factor * factor;
+            }
+            __syncthreads();  // sh_max is used again below
+        }
+        const float rstd = 1.0f / sqrtf(square);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int ch = c * threads + t;
@@ -175,7 +226,7 @@ __global__ __launch_bounds__(kRowThreads) void int8_rows_kernel(Rows p)
                     load8<WT>(p.a.weight, static_cast<size_t>(ch) * kVec, w);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
-                    v[c][i] = v[c][i] * rstd * (p.a.weight_offset + w[i]);
+                    v[c][i] = v[c][i] * factor * rstd * (p.a.weight_offset + w[i]);
                 if (p.a.y_out)
                     store8<T>(p.a.y_out, at, v[c]);
             }
