@@ -251,20 +251,23 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _record(stream, *tensors) -> None:
-    """Tensors allocated inside a binding belong to the current stream's
-    pool; when the call was enqueued on another stream, mark them as used
-    there so the caching allocator cannot hand their memory out again before
-    that stream's kernels are done."""
-    if stream is None:
-        return
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on `stream` to write. On a stream other than the
+    current one it comes from that stream's pool: memory of the current
+    stream's pool may still be in use by what the caller enqueued there before,
+    which `stream` does not wait for. It is marked as used on the current
+    stream too, so that a caller may go on with it there (having waited for
+    `stream`) and drop it."""
     import torch
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    if int(s.cuda_stream) == int(torch.cuda.current_stream().cuda_stream):
-        return
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        current = torch.cuda.current_stream()
+        if int(s.cuda_stream) != int(current.cuda_stream):
+            with torch.cuda.stream(s):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            t.record_stream(current)
+            return t
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _check_tensor(t, dtype, shape, name, device=None):
@@ -311,20 +314,17 @@ def forward(x, gate: DeviceWeight, up: DeviceWeight, down: DeviceWeight, act: in
     _check_nvfp4_weight(gate, N, K, "gate", x.device)
     _check_nvfp4_weight(up, N, K, "up", x.device)
     _check_nvfp4_weight(down, K, N, "down", x.device)
-    new_out = out is None
-    if new_out:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+    if out is None:
+        out = _empty((M, K), torch.bfloat16, x.device, stream)
     _check_tensor(out, torch.bfloat16, (M, K), "out", x.device)
     need = workspace_bytes(M, K, N)
-    new_ws = workspace is None
-    if new_ws:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+    if workspace is None:
+        workspace = _empty(max(need, 1), torch.uint8, x.device, stream)
     g, u, d = gate.struct(), up.struct(), down.struct()
     rc = load().ffn_nvfp4_forward(x.data_ptr(), M, K, N, ctypes.byref(g), ctypes.byref(u), ctypes.byref(d),
                                   int(act), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                   out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_nvfp4_forward")
-    _record(stream, out if new_out else None, workspace if new_ws else None)
     return out
 
 
@@ -356,18 +356,16 @@ def dual_gemv(x, gate: DeviceWeight, up: DeviceWeight, gate_out=None, up_out=Non
     _check_tensor(x, torch.bfloat16, (M, K), "x")
     _check_nvfp4_weight(gate, N, K, "gate", x.device)
     _check_nvfp4_weight(up, N, K, "up", x.device)
-    new_g, new_u = gate_out is None, up_out is None
-    if new_g:
-        gate_out = torch.empty((M, N), dtype=torch.float32, device=x.device)
-    if new_u:
-        up_out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+    if gate_out is None:
+        gate_out = _empty((M, N), torch.float32, x.device, stream)
+    if up_out is None:
+        up_out = _empty((M, N), torch.float32, x.device, stream)
     _check_tensor(gate_out, torch.float32, (M, N), "gate_out", x.device)
     _check_tensor(up_out, torch.float32, (M, N), "up_out", x.device)
     g, u = gate.struct(), up.struct()
     rc = load().ffn_nvfp4_dual_gemv(x.data_ptr(), M, K, N, ctypes.byref(g), ctypes.byref(u),
                                     gate_out.data_ptr(), up_out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_nvfp4_dual_gemv")
-    _record(stream, gate_out if new_g else None, up_out if new_u else None)
     return gate_out, up_out
 
 
@@ -380,15 +378,13 @@ def down_gemv(gate_in, up_in, down: DeviceWeight, act: int = ACT_SILU, out=None,
     _check_tensor(gate_in, torch.float32, (M, N), "gate_in")
     _check_tensor(up_in, torch.float32, (M, N), "up_in", gate_in.device)
     _check_nvfp4_weight(down, K, N, "down", gate_in.device)
-    new_out = out is None
-    if new_out:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=gate_in.device)
+    if out is None:
+        out = _empty((M, K), torch.bfloat16, gate_in.device, stream)
     _check_tensor(out, torch.bfloat16, (M, K), "out", gate_in.device)
     d = down.struct()
     rc = load().ffn_nvfp4_down_gemv(gate_in.data_ptr(), up_in.data_ptr(), M, N, K, ctypes.byref(d), int(act),
                                     out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_nvfp4_down_gemv")
-    _record(stream, out if new_out else None)
     return out
 
 
@@ -403,28 +399,22 @@ def quantize(w, codes=None, scales=None, scale2=None, workspace=None, stream=Non
     rows, cols = w.shape
     _check_tensor(w, torch.bfloat16, (rows, cols), "w")
     dev = w.device
-    fresh = []
     if codes is None:
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
-        fresh.append(codes)
+        codes = _empty((rows, cols // 2), torch.uint8, dev, stream)
     if scales is None:
-        scales = torch.empty((rows, cols // 16), dtype=torch.uint8, device=dev)
-        fresh.append(scales)
+        scales = _empty((rows, cols // 16), torch.uint8, dev, stream)
     if scale2 is None:
-        scale2 = torch.empty(1, dtype=torch.float32, device=dev)
-        fresh.append(scale2)
+        scale2 = _empty(1, torch.float32, dev, stream)
     _check_tensor(codes, torch.uint8, (rows, cols // 2), "codes", dev)
     _check_tensor(scales, torch.uint8, (rows, cols // 16), "scales", dev)
     _check_tensor(scale2, torch.float32, (1,), "scale2", dev)
     need = quantize_workspace_bytes(rows, cols)
     if workspace is None:
-        workspace = torch.empty(max(need, 4), dtype=torch.uint8, device=dev)
-        fresh.append(workspace)
+        workspace = _empty(max(need, 4), torch.uint8, dev, stream)
     rc = load().ffn_nvfp4_quantize(w.data_ptr(), rows, cols, codes.data_ptr(), scales.data_ptr(),
                                    scale2.data_ptr(), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check(rc, "ffn_nvfp4_quantize")
-    _record(stream, *fresh)
     return codes, scales, scale2
 
 
@@ -498,20 +488,17 @@ def fp8_forward(x, gate: Fp8DeviceWeight, up: Fp8DeviceWeight, down: Fp8DeviceWe
     _check_fp8_weight(gate, N, K, "gate", x.device)
     _check_fp8_weight(up, N, K, "up", x.device)
     _check_fp8_weight(down, K, N, "down", x.device)
-    new_out = out is None
-    if new_out:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+    if out is None:
+        out = _empty((M, K), torch.bfloat16, x.device, stream)
     _check_tensor(out, torch.bfloat16, (M, K), "out", x.device)
     need = fp8_workspace_bytes(M, K, N)
-    new_ws = workspace is None
-    if new_ws:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+    if workspace is None:
+        workspace = _empty(max(need, 1), torch.uint8, x.device, stream)
     g, u, d = gate.struct(), up.struct(), down.struct()
     rc = load().ffn_fp8_forward(x.data_ptr(), M, K, N, ctypes.byref(g), ctypes.byref(u), ctypes.byref(d),
                                 int(act), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                 out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_fp8_forward")
-    _record(stream, out if new_out else None, workspace if new_ws else None)
     return out
 
 
@@ -523,18 +510,16 @@ def fp8_dual_gemv(x, gate: Fp8DeviceWeight, up: Fp8DeviceWeight, gate_out=None, 
     _check_tensor(x, torch.bfloat16, (M, K), "x")
     _check_fp8_weight(gate, N, K, "gate", x.device)
     _check_fp8_weight(up, N, K, "up", x.device)
-    new_g, new_u = gate_out is None, up_out is None
-    if new_g:
-        gate_out = torch.empty((M, N), dtype=torch.float32, device=x.device)
-    if new_u:
-        up_out = torch.empty((M, N), dtype=torch.float32, device=x.device)
+    if gate_out is None:
+        gate_out = _empty((M, N), torch.float32, x.device, stream)
+    if up_out is None:
+        up_out = _empty((M, N), torch.float32, x.device, stream)
     _check_tensor(gate_out, torch.float32, (M, N), "gate_out", x.device)
     _check_tensor(up_out, torch.float32, (M, N), "up_out", x.device)
     g, u = gate.struct(), up.struct()
     rc = load().ffn_fp8_dual_gemv(x.data_ptr(), M, K, N, ctypes.byref(g), ctypes.byref(u),
                                   gate_out.data_ptr(), up_out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_fp8_dual_gemv")
-    _record(stream, gate_out if new_g else None, up_out if new_u else None)
     return gate_out, up_out
 
 
@@ -547,15 +532,13 @@ def fp8_down_gemv(gate_in, up_in, down: Fp8DeviceWeight, act: int = ACT_SILU, ou
     _check_tensor(gate_in, torch.float32, (M, N), "gate_in")
     _check_tensor(up_in, torch.float32, (M, N), "up_in", gate_in.device)
     _check_fp8_weight(down, K, N, "down", gate_in.device)
-    new_out = out is None
-    if new_out:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=gate_in.device)
+    if out is None:
+        out = _empty((M, K), torch.bfloat16, gate_in.device, stream)
     _check_tensor(out, torch.bfloat16, (M, K), "out", gate_in.device)
     d = down.struct()
     rc = load().ffn_fp8_down_gemv(gate_in.data_ptr(), up_in.data_ptr(), M, N, K, ctypes.byref(d), int(act),
                                   out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_fp8_down_gemv")
-    _record(stream, out if new_out else None)
     return out
 
 
@@ -599,13 +582,12 @@ def w4a4_prepare_weight(w: DeviceWeight, stream=None) -> MxDeviceWeight:
     rows, cols = w.rows, w.cols
     dev = w.codes.device
     _check_nvfp4_weight(w, rows, cols, "w", dev)
-    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+    codes = _empty((rows, cols // 2), torch.uint8, dev, stream)
+    scales = _empty((rows, cols // 32), torch.uint8, dev, stream)
     st = w.struct()
     rc = load().ffn_w4a4_prepare_weight(ctypes.byref(st), rows, cols, codes.data_ptr(), scales.data_ptr(),
                                         _stream_handle(stream))
     _check(rc, "ffn_w4a4_prepare_weight")
-    _record(stream, codes, scales)
     return MxDeviceWeight(codes, scales, float(w.scale2))
 
 
@@ -622,24 +604,19 @@ def w4a4_dual_gemm(x, gate: MxDeviceWeight, up: MxDeviceWeight, gate_out=None, u
     _check_tensor(x, torch.bfloat16, (M, K), "x")
     _check_mx_weight(gate, N, K, "gate", x.device)
     _check_mx_weight(up, N, K, "up", x.device)
-    fresh = []
     if gate_out is None:
-        gate_out = torch.empty((M, N), dtype=torch.float32, device=x.device)
-        fresh.append(gate_out)
+        gate_out = _empty((M, N), torch.float32, x.device, stream)
     if up_out is None:
-        up_out = torch.empty((M, N), dtype=torch.float32, device=x.device)
-        fresh.append(up_out)
+        up_out = _empty((M, N), torch.float32, x.device, stream)
     _check_tensor(gate_out, torch.float32, (M, N), "gate_out", x.device)
     _check_tensor(up_out, torch.float32, (M, N), "up_out", x.device)
     if workspace is None:
-        workspace = torch.empty(max(w4a4_workspace_bytes(M, K, N), 1), dtype=torch.uint8, device=x.device)
-        fresh.append(workspace)
+        workspace = _empty(max(w4a4_workspace_bytes(M, K, N), 1), torch.uint8, x.device, stream)
     g, u = gate.struct(), up.struct()
     rc = load().ffn_w4a4_dual_gemm(x.data_ptr(), M, K, N, ctypes.byref(g), ctypes.byref(u), gate_out.data_ptr(),
                                    up_out.data_ptr(), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check(rc, "ffn_w4a4_dual_gemm")
-    _record(stream, *fresh)
     return gate_out, up_out
 
 
@@ -653,20 +630,16 @@ def w4a4_forward(x, gate: MxDeviceWeight, up: MxDeviceWeight, down: DeviceWeight
     _check_mx_weight(gate, N, K, "gate", x.device)
     _check_mx_weight(up, N, K, "up", x.device)
     _check_nvfp4_weight(down, K, N, "down", x.device)
-    fresh = []
     if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
-        fresh.append(out)
+        out = _empty((M, K), torch.bfloat16, x.device, stream)
     _check_tensor(out, torch.bfloat16, (M, K), "out", x.device)
     if workspace is None:
-        workspace = torch.empty(max(w4a4_workspace_bytes(M, K, N), 1), dtype=torch.uint8, device=x.device)
-        fresh.append(workspace)
+        workspace = _empty(max(w4a4_workspace_bytes(M, K, N), 1), torch.uint8, x.device, stream)
     g, u, d = gate.struct(), up.struct(), down.struct()
     rc = load().ffn_w4a4_forward(x.data_ptr(), M, K, N, ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), int(act),
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(),
                                  _stream_handle(stream))
     _check(rc, "ffn_w4a4_forward")
-    _record(stream, *fresh)
     return out
 
 
@@ -682,19 +655,15 @@ def w4a4_down_gemm(h, down: MxDeviceWeight, out=None, workspace=None, stream=Non
     K = down.rows
     _check_tensor(h, torch.bfloat16, (M, N), "h")
     _check_mx_weight(down, K, N, "down", h.device)
-    fresh = []
     if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=h.device)
-        fresh.append(out)
+        out = _empty((M, K), torch.bfloat16, h.device, stream)
     _check_tensor(out, torch.bfloat16, (M, K), "out", h.device)
     if workspace is None:
-        workspace = torch.empty(max(w4a4_fp4_workspace_bytes(M, K, N), 1), dtype=torch.uint8, device=h.device)
-        fresh.append(workspace)
+        workspace = _empty(max(w4a4_fp4_workspace_bytes(M, K, N), 1), torch.uint8, h.device, stream)
     d = down.struct()
     rc = load().ffn_w4a4_down_gemm(h.data_ptr(), M, N, K, ctypes.byref(d), out.data_ptr(), workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check(rc, "ffn_w4a4_down_gemm")
-    _record(stream, *fresh)
     return out
 
 
@@ -709,20 +678,16 @@ def w4a4_forward_fp4(x, gate: MxDeviceWeight, up: MxDeviceWeight, down: MxDevice
     _check_mx_weight(gate, N, K, "gate", x.device)
     _check_mx_weight(up, N, K, "up", x.device)
     _check_mx_weight(down, K, N, "down", x.device)
-    fresh = []
     if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
-        fresh.append(out)
+        out = _empty((M, K), torch.bfloat16, x.device, stream)
     _check_tensor(out, torch.bfloat16, (M, K), "out", x.device)
     if workspace is None:
-        workspace = torch.empty(max(w4a4_fp4_workspace_bytes(M, K, N), 1), dtype=torch.uint8, device=x.device)
-        fresh.append(workspace)
+        workspace = _empty(max(w4a4_fp4_workspace_bytes(M, K, N), 1), torch.uint8, x.device, stream)
     g, u, d = gate.struct(), up.struct(), down.struct()
     rc = load().ffn_w4a4_forward_fp4(x.data_ptr(), M, K, N, ctypes.byref(g), ctypes.byref(u), ctypes.byref(d),
                                      int(act), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                      out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_w4a4_forward_fp4")
-    _record(stream, *fresh)
     return out
 
 
@@ -803,21 +768,17 @@ def int8_rmsnorm(x, weight, eps: float = 1e-6, residual=None, weight_offset: flo
     _check_tensor(weight, weight.dtype, (K,), "weight", dev)
     if residual is not None:
         _check_tensor(residual, x.dtype, (M, K), "residual", dev)
-    fresh = []
     if codes is None:
-        codes = torch.empty((M, K), dtype=torch.int8, device=dev)
-        fresh.append(codes)
+        codes = _empty((M, K), torch.int8, dev, stream)
     else:
         _check_tensor(codes, torch.int8, (M, K), "codes", dev)
     if scales is None:
-        scales = torch.empty(M, dtype=torch.float32, device=dev)
-        fresh.append(scales)
+        scales = _empty(M, torch.float32, dev, stream)
     else:
         _check_tensor(scales, torch.float32, (M,), "scales", dev)
     if sum_out is None:
         if residual is not None:
-            sum_out = torch.empty((M, K), dtype=x.dtype, device=dev)
-            fresh.append(sum_out)
+            sum_out = _empty((M, K), x.dtype, dev, stream)
     else:
         _check_tensor(sum_out, x.dtype, (M, K), "sum_out", dev)
     if y_out is not None:
@@ -827,7 +788,6 @@ def int8_rmsnorm(x, weight, eps: float = 1e-6, residual=None, weight_offset: flo
                                  None if sum_out is None else sum_out.data_ptr(),
                                  None if y_out is None else y_out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_int8_rmsnorm")
-    _record(stream, *fresh)
     return codes, scales, sum_out
 
 
@@ -838,21 +798,17 @@ def int8_quantize(x, codes=None, scales=None, stream=None):
     dtype = _int8_dtype(x.dtype, "x")
     dev = x.device
     _check_tensor(x, x.dtype, (rows, cols), "x")
-    fresh = []
     if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
-        fresh.append(codes)
+        codes = _empty((rows, cols), torch.int8, dev, stream)
     else:
         _check_tensor(codes, torch.int8, (rows, cols), "codes", dev)
     if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=dev)
-        fresh.append(scales)
+        scales = _empty(rows, torch.float32, dev, stream)
     else:
         _check_tensor(scales, torch.float32, (rows,), "scales", dev)
     rc = load().ffn_int8_quantize(x.data_ptr(), rows, cols, dtype, codes.data_ptr(), scales.data_ptr(),
                                   _stream_handle(stream))
     _check(rc, "ffn_int8_quantize")
-    _record(stream, *fresh)
     return codes, scales
 
 
@@ -867,13 +823,12 @@ def int8_prepare_weight(w: DeviceWeight, stream=None) -> Int8DeviceWeight:
     rows, cols = w.rows, w.cols
     dev = w.codes.device
     _check_nvfp4_weight(w, rows, cols, "w", dev)
-    codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
-    scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    codes = _empty((rows, cols), torch.int8, dev, stream)
+    scales = _empty(rows, torch.float32, dev, stream)
     st = w.struct()
     rc = load().ffn_int8_prepare_weight(ctypes.byref(st), rows, cols, codes.data_ptr(), scales.data_ptr(),
                                         _stream_handle(stream))
     _check(rc, "ffn_int8_prepare_weight")
-    _record(stream, codes, scales)
     return Int8DeviceWeight(codes, scales)
 
 
@@ -896,18 +851,15 @@ def int8_gemm(xq, xs, w: Int8DeviceWeight, bias=None, out_dtype=None, out=None, 
     if out_dtype is None:
         out_dtype = torch.bfloat16 if out is None else out.dtype
     dtype = _int8_dtype(out_dtype, "out")
-    fresh = []
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        fresh.append(out)
+        out = _empty((M, N), out_dtype, dev, stream)
     else:
         _check_tensor(out, out_dtype, (M, N), "out", dev)
     lib = load()
     need = lib.ffn_int8_gemm_workspace_bytes(M, K, N)
     if workspace is None:
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            fresh.append(workspace)
+            workspace = _empty(need, torch.uint8, dev, stream)
     else:
         _check_workspace(workspace, dev)
     st = w.struct()
@@ -917,7 +869,6 @@ def int8_gemm(xq, xs, w: Int8DeviceWeight, bias=None, out_dtype=None, out=None, 
                            0 if workspace is None else workspace.numel() * workspace.element_size(),
                            _stream_handle(stream))
     _check(rc, "ffn_int8_gemm")
-    _record(stream, *fresh)
     return out
 
 
@@ -936,22 +887,18 @@ def int8_dual_gemm(xq, xs, gate: Int8DeviceWeight, up: Int8DeviceWeight, act: in
     _check_tensor(xs, torch.float32, (M,), "xs", dev)
     _check_int8_weight(gate, N, K, "gate", dev)
     _check_int8_weight(up, N, K, "up", dev)
-    fresh = []
     if hq is None:
-        hq = torch.empty((M, N), dtype=torch.int8, device=dev)
-        fresh.append(hq)
+        hq = _empty((M, N), torch.int8, dev, stream)
     else:
         _check_tensor(hq, torch.int8, (M, N), "hq", dev)
     if hs is None:
-        hs = torch.empty(M, dtype=torch.float32, device=dev)
-        fresh.append(hs)
+        hs = _empty(M, torch.float32, dev, stream)
     else:
         _check_tensor(hs, torch.float32, (M,), "hs", dev)
     lib = load()
     need = lib.ffn_int8_workspace_bytes(M, K, N)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        fresh.append(workspace)
+        workspace = _empty(max(need, 1), torch.uint8, dev, stream)
     else:
         _check_workspace(workspace, dev)
     g, u = gate.struct(), up.struct()
@@ -959,7 +906,6 @@ def int8_dual_gemm(xq, xs, gate: Int8DeviceWeight, up: Int8DeviceWeight, act: in
                                 hq.data_ptr(), hs.data_ptr(), workspace.data_ptr(),
                                 workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check(rc, "ffn_int8_dual_gemm")
-    _record(stream, *fresh)
     return hq, hs
 
 
@@ -979,17 +925,14 @@ def int8_forward(xq, xs, gate: Int8DeviceWeight, up: Int8DeviceWeight, down: Int
     if out_dtype is None:
         out_dtype = torch.bfloat16 if out is None else out.dtype
     dtype = _int8_dtype(out_dtype, "out")
-    fresh = []
     if out is None:
-        out = torch.empty((M, K), dtype=out_dtype, device=dev)
-        fresh.append(out)
+        out = _empty((M, K), out_dtype, dev, stream)
     else:
         _check_tensor(out, out_dtype, (M, K), "out", dev)
     lib = load()
     need = lib.ffn_int8_workspace_bytes(M, K, N)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        fresh.append(workspace)
+        workspace = _empty(max(need, 1), torch.uint8, dev, stream)
     else:
         _check_workspace(workspace, dev)
     g, u, d = gate.struct(), up.struct(), down.struct()
@@ -997,7 +940,6 @@ def int8_forward(xq, xs, gate: Int8DeviceWeight, up: Int8DeviceWeight, down: Int
                               ctypes.byref(d), int(act), dtype, workspace.data_ptr(),
                               workspace.numel() * workspace.element_size(), out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_int8_forward")
-    _record(stream, *fresh)
     return out
 
 
