@@ -130,3 +130,42 @@ def test_freed_memory_of_the_current_stream_is_not_taken():
         assert float(total) == 3.0 * 4096 * 4096
         assert torch.equal(codes, again[0]) and torch.equal(scales, again[1])
         del codes, scales
+
+
+def test_quantize_weight_reads_scale2_on_the_calls_stream(monkeypatch):
+    """The read back to the host waits for the stream that writes scale2, not for the current one."""
+    current, side = Stream(1), Stream(2)
+    active, seen = [current], []
+
+    @contextlib.contextmanager
+    def on(s):
+        active.append(s)
+        yield
+        active.pop()
+
+    class Scale:
+        def cpu(self):
+            seen.append(active[-1])
+            return [0.5]
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: active[-1])
+    monkeypatch.setattr(ffn, "quantize", lambda w, stream=None: ("codes", "scales", Scale()))
+    for s in (side, None):
+        assert ffn.quantize_weight(None, stream=s).scale2 == 0.5
+    assert seen == [side, current]
+
+
+@pytest.mark.gpu
+def test_quantize_weight_on_a_busy_stream():
+    w = (torch.randn(1024, 2048, device="cuda") * 0.02).to(BF)
+    ref = ffn.quantize_weight(w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = ffn.quantize_weight(w, stream=side)
+        assert got.scale2 == ref.scale2
+        assert torch.equal(got.codes, ref.codes) and torch.equal(got.scales, ref.scales)

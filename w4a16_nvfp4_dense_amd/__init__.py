@@ -251,6 +251,12 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _torch_stream(stream):
+    """A stream argument (a torch stream or a raw handle) as a torch stream."""
+    import torch
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+
+
 def _empty(shape, dtype, device, stream):
     """A tensor for a call on `stream` to write. On a stream other than the
     current one it comes from that stream's pool: memory of the current
@@ -260,7 +266,7 @@ def _empty(shape, dtype, device, stream):
     `stream`) and drop it."""
     import torch
     if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        s = _torch_stream(stream)
         current = torch.cuda.current_stream()
         if int(s.cuda_stream) != int(current.cuda_stream):
             with torch.cuda.stream(s):
@@ -419,10 +425,16 @@ def quantize(w, codes=None, scales=None, scale2=None, workspace=None, stream=Non
 
 
 def quantize_weight(w, stream=None) -> DeviceWeight:
-    """:func:`quantize` as a DeviceWeight (waits for the result to read
-    scale2 back to the host)."""
+    """:func:`quantize` as a DeviceWeight (waits for the result, on the call's
+    stream, to read scale2 back to the host)."""
+    import torch
     codes, scales, scale2 = quantize(w, stream=stream)
-    return DeviceWeight(codes, scales, float(scale2.cpu()[0]))
+    if stream is None:
+        value = scale2.cpu()
+    else:
+        with torch.cuda.stream(_torch_stream(stream)):
+            value = scale2.cpu()
+    return DeviceWeight(codes, scales, float(value[0]))
 
 
 def bf16_from_bits(bits, device="cuda"):
