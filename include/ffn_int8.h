@@ -42,6 +42,8 @@
  *   - matrices of codes or values, and workspaces, are 16-byte aligned; fp32
  *     vectors (scales, bias) 4-byte aligned (else FFN_NVFP4_ERR_ALIGN).
  *   - an unknown type is FFN_NVFP4_ERR_ACT.
+ *   - outputs and workspaces overlap no other buffer of the call, unless an
+ *     entry says otherwise.
  */
 #ifndef FFN_INT8_H
 #define FFN_INT8_H
@@ -86,9 +88,11 @@ typedef struct ffn_int8_weight {
  *              has no norm: its y is NaN
  *   codes      device int8 [M, K] (written); scales: device fp32 [M] (written)
  *   sum_out    device [M, K] of `dtype` (written), or NULL; may be x or
- *              residual itself, no other overlap
- *   y_out      device [M, K] of `dtype` (written), or NULL; as sum_out, and
- *              not the same buffer */
+ *              residual itself
+ *   y_out      device [M, K] of `dtype` (written), or NULL; may be x or
+ *              residual itself, not sum_out
+ * Any other overlap of what is written with another buffer is
+ * FFN_NVFP4_ERR_ALIAS. */
 int ffn_int8_rmsnorm(const void *x, const void *residual, const void *weight, int M, int K, int dtype,
                      int weight_dtype, float eps, float weight_offset, int8_t *codes, float *scales,
                      void *sum_out, void *y_out, hipStream_t stream);

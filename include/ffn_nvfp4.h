@@ -70,6 +70,7 @@ extern "C" {
 #define FFN_NVFP4_ERR_WORKSPACE (-6)     /* workspace smaller than ffn_nvfp4_workspace_bytes() */
 #define FFN_NVFP4_ERR_LAUNCH (-7)        /* HIP reported an error when launching */
 #define FFN_NVFP4_ERR_SCALE2 (-8)        /* scale2 is not finite */
+#define FFN_NVFP4_ERR_ALIAS (-9)         /* buffers overlap in a way the entry refuses */
 
 /* Activation of the gate. SiLU(g) = g / (1 + e^-g) (Qwen/Llama);
  * GELU-tanh(g) = 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) (Gemma).

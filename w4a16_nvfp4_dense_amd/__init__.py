@@ -76,6 +76,7 @@ ERR_ACT = -5
 ERR_WORKSPACE = -6
 ERR_LAUNCH = -7
 ERR_SCALE2 = -8
+ERR_ALIAS = -9
 
 
 class FfnError(RuntimeError):

@@ -230,6 +230,7 @@ const char *ffn_nvfp4_strerror(int status)
     case FFN_NVFP4_ERR_WORKSPACE: return "workspace too small";
     case FFN_NVFP4_ERR_LAUNCH: return "kernel launch failed";
     case FFN_NVFP4_ERR_SCALE2: return "scale2 is not finite";
+    case FFN_NVFP4_ERR_ALIAS: return "buffers overlap";
     default: return "unknown status";
     }
 }

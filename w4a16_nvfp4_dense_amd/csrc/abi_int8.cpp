@@ -73,6 +73,23 @@ size_t round256(size_t b)
     return (b + 255) & ~static_cast<size_t>(255);
 }
 
+size_t dtype_bytes(int t)
+{
+    return t == FFN_INT8_F32 ? 4 : 2;
+}
+
+// A buffer of a call. (A null one overlaps nothing.)
+struct Span {
+    const void *p;
+    size_t bytes;
+};
+
+bool overlap(const Span &a, const Span &b)
+{
+    const uintptr_t i = reinterpret_cast<uintptr_t>(a.p), j = reinterpret_cast<uintptr_t>(b.p);
+    return i && j && i < j + b.bytes && j < i + a.bytes;
+}
+
 ffn::Int8Out out_kind(int dtype)
 {
     return dtype == FFN_INT8_BF16 ? ffn::I8_BF16 : dtype == FFN_INT8_F16 ? ffn::I8_F16 : ffn::I8_F32;
@@ -149,6 +166,22 @@ int ffn_int8_rmsnorm(const void *x, const void *residual, const void *weight, in
     if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(codes, 16) || !aligned(scales, 4) ||
         !aligned(sum_out, 16) || !aligned(y_out, 16))
         return FFN_NVFP4_ERR_ALIGN;
+    // A row is in registers before any of it is written, so x or residual may be
+    // written in place; rows that overlap others would be read after that.
+    const size_t elements = static_cast<size_t>(M) * static_cast<size_t>(K);
+    const size_t real = elements * dtype_bytes(dtype);
+    const Span in[] = {{x, real}, {residual, real}, {weight, static_cast<size_t>(K) * dtype_bytes(weight_dtype)}};
+    const Span out[] = {{sum_out, real}, {y_out, real}, {codes, elements}, {scales, 4 * static_cast<size_t>(M)}};
+    for (int o = 0; o < 4; ++o) {
+        for (int i = 0; i < 3; ++i) {
+            const bool in_place = o < 2 && i < 2 && out[o].p == in[i].p;
+            if (!in_place && overlap(out[o], in[i]))
+                return FFN_NVFP4_ERR_ALIAS;
+        }
+        for (int other = 0; other < o; ++other)
+            if (overlap(out[o], out[other]))
+                return FFN_NVFP4_ERR_ALIAS;
+    }
     const ffn::Int8RowsArgs a{x, residual, weight, M, K, eps, weight_offset, codes, scales, sum_out, y_out};
     return launch_status(ffn::launch_int8_rmsnorm(a, dtype, weight_dtype, stream));
 }
