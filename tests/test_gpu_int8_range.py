@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import w4a16_nvfp4_dense_amd as ffn
-from test_gpu_int8 import TORCH, check_norm, norm64, np_of, rounded, same_bits
+from test_gpu_int8 import check_norm, norm64, np_of, rounded, same_bits
 
 pytestmark = pytest.mark.gpu
 
