@@ -112,7 +112,7 @@ typedef struct ffn_nvfp4_weight {
 /* Bytes of device workspace ffn_nvfp4_forward needs for (M, K, N);
  * 0 if M = 0 or the shape is unsupported. For M <= 8 it holds h [M, N] bf16;
  * for the small-batch arm h, the fp32 partial sums of split reductions and
- * their ready words (about 23 MB at M = 40, K = 5120, N = 17408, mostly the
+ * the words that count them (about 23 MB at M = 40, K = 5120, N = 17408, mostly the
  * dual projection's partial sums);
  * for the 128-row arm, h for one block of up to 128 rows plus the fp32 slots
  * in which that arm leaves the pieces of split reductions (about 64 MiB,

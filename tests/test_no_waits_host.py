@@ -1,0 +1,16 @@
+"""No kernel waits for another workgroup (host only: read from the sources). One that waits holds a compute unit that
+the one it waits for may need while other launches hold the rest."""
+import os
+
+import pytest
+
+import w4a16_nvfp4_dense_amd as ffn
+
+CSRC = os.path.join(ffn.PKG_DIR, "csrc")
+
+
+@pytest.mark.parametrize("name", ["smallm_gemm.h"])
+def test_no_wait(name):
+    with open(os.path.join(CSRC, name)) as f:
+        text = f.read()
+    assert "wait_ready" not in text and "s_sleep" not in text

@@ -7,13 +7,8 @@
 // tile may be shared by neighbouring workgroups, each with one part of its
 // stages. A workgroup walks its share downwards.
 //
-// No workgroup ever waits for another. A shared tile has one word in the
-// workspace, the launch's tag with the count of the parts whose sums are in the
-// workspace. A workgroup writes its part's sums, then counts itself there; the
-// one that finds all others counted adds their sums to its own and stores the
-// tile. Whichever that is, and in whatever order and however late the
-// workgroups of a launch run beside those of other launches, every tile is
-// finished exactly once, after all its parts are there.
+// No workgroup ever waits for another: a shared tile is finished by the one that
+// counts itself last in the tile's word (shared_word.h).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -21,6 +16,8 @@
 #include <stdint.h>
 
 #include <algorithm>
+
+#include "shared_word.h"
 
 namespace ffn {
 
@@ -151,40 +148,6 @@ struct Cursor {
         return true;
     }
 };
-
-// ------------------------------------------------------- the word of a tile
-// The low bits count parts, the rest is the launch's tag. A word of any other
-// tag (what the workspace held before, or zero) stands for no parts: the first
-// part replaces it. The workgroup that finishes the tile sets it to zero, by
-// then being the only one left that uses it, so that a replay of the same launch
-// starts afresh.
-constexpr int kCountBits = 16;  // more than a tile has stages, so than parts
-
-__host__ __device__ __forceinline__ unsigned long long tag_of_launch(unsigned long long number)
-{
-    const unsigned long long tag = number >> kCountBits << kCountBits;
-    return tag ? tag : 1ull << kCountBits;
-}
-
-__host__ __device__ __forceinline__ bool is_tagged(unsigned long long word, unsigned long long tag)
-{
-    return word >> kCountBits == tag >> kCountBits;
-}
-
-// Counts one part in the word; returns how many it holds now. `seen` is what
-// the word may hold (a guess costs one more try). Word: exchange(seen, next)
-// sets the word to `next` if it holds `seen`, else writes what it holds to
-// `seen` and returns false; add_one() returns what the word held. Ends: a word
-// that is tagged stays so until this part is counted, so exchange fails at most
-// twice, for a wrong guess and for another first part.
-template <class Word>
-__host__ __device__ __forceinline__ int count_part(Word &word, unsigned long long tag, unsigned long long seen)
-{
-    while (!is_tagged(seen, tag))
-        if (word.exchange(seen, tag + 1))
-            return 1;
-    return static_cast<int>(word.add_one() - tag) + 1;
-}
 
 // ---------------------------------------------------------------- the launch
 struct Plan {

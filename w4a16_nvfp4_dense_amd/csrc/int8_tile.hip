@@ -71,28 +71,6 @@ __device__ __forceinline__ int piece_swizzle(int i)
     return (i >> 1) & 7;
 }
 
-// A word of the workspace that workgroups on any XCD count in.
-struct SharedWord {
-    unsigned long long *at;
-    __device__ __forceinline__ bool exchange(unsigned long long &seen, unsigned long long next) const
-    {
-        return __hip_atomic_compare_exchange_strong(at, &seen, next, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
-                                                    __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __device__ __forceinline__ unsigned long long add_one() const
-    {
-        return __hip_atomic_fetch_add(at, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __device__ __forceinline__ unsigned long long load() const
-    {
-        return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __device__ __forceinline__ void clear() const
-    {
-        __hip_atomic_store(at, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-};
-
 // The matrix instruction on fragments of F tokens x F channels (F = 16: 64
 // columns at a time, F = 32: 32 columns). Lane l holds row l % F of either
 // operand and the 16 bytes at piece l / F of a step; group g of its results

@@ -54,13 +54,12 @@
 // tiles [g T / G, (g + 1) T / G) with g = w / P, T tiles and G = gridDim / P
 // groups. With P = 1 the epilogue writes finished outputs. With P > 1
 // (SPLIT) every workgroup stores its part's fp32 sums of its tiles with
-// device-coherent stores; the lower parts' workgroups then set their ready
-// words, and the last part's workgroup (the highest id of the P, so it waits
-// only for workgroups dispatched before it, which wait for nobody) adds the
-// parts in order, part 0 first, and runs the epilogue. (A first version that
-// let the last workgroup to finish add the parts, behind device-scope
-// release/acquire fences, measured slower than a separate reduction launch:
-// the fences write back and invalidate the XCD's L2.) The order of every sum
+// device-coherent stores and counts itself in its group's word (shared_word.h);
+// the one that finds the other parts counted adds the parts in order, part 0
+// first, and runs the epilogue. No workgroup waits for another. (Device-scope
+// release/acquire fences around the counting, instead of coherent stores and
+// loads, measured slower than a separate reduction launch: they write back and
+// invalidate the XCD's L2.) The order of every sum
 // is fixed, and a token row's result does not depend on the other rows of the
 // batch within one token-group count (the count sets the parts, hence the
 // order of the sums).
@@ -68,6 +67,7 @@
 
 #include "kernels.h"
 #include "nvfp4_device.h"
+#include "shared_word.h"
 
 namespace ffn {
 
@@ -99,8 +99,8 @@ struct SmallParams {
     int groups;  // G: workgroups per part
     float *part0;  // P x [M, rows] fp32 pieces of the first projection (split reductions)
     float *part1;  // the same for the second projection
-    unsigned long long *flags;  // one ready word per workgroup (split reductions)
-    unsigned long long tag;     // this launch's ready value (nonzero)
+    unsigned long long *flags;  // a word for each group of row tiles (split reductions)
+    unsigned long long tag;     // this launch's tag for them
 };
 
 // LDS of one ring stage: codes [NMAT][2 row halves][4 column blocks][8 rows]
@@ -408,28 +408,24 @@ __global__ __launch_bounds__(kSmWaves * 64) void smallm_gemm_kernel(const SmallP
         // The P workgroups blockIdx.x - part .. + P - 1 hold the parts of the
         // same tiles. Every wave waits for its own piece stores (nothing else
         // it issued matters: the ring's trailing loads only fill LDS); once
-        // all have, a lower part's workgroup publishes its pieces.
+        // all have, the workgroup counts its pieces.
         wait_vmcnt<0>();
         __syncthreads();
-        if (part != P - 1) {
-            if (q == 0)
-                __hip_atomic_store(p.flags + blockIdx.x, p.tag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            return;
+        FFN_LDS int *counted = (FFN_LDS int *)red;  // (the last tile's sums are read)
+        if (tid == 0) {
+            const SharedWord word{p.flags + grp};
+            const int n = count_part(word, p.tag, 0);
+            if (n == P)
+                word.clear();
+            *counted = n;
         }
-        // The last part's workgroup finishes the tiles: thread (q, lane) takes
-        // element (token 16 t + tid2 / 16, row tid2 % 16) with tid2 = 64 (q %
-        // 4) + lane of the (tile, token group) items q / 4, q / 4 + 4, ... It
-        // waits only for lower-numbered workgroups, which were dispatched
-        // first and wait for nobody.
-        const int g0 = blockIdx.x - part;
-        // (one word at a time: polling all of them at once measured no faster)
-        for (int pp = 0; pp < P - 1; ++pp)
-            wait_ready([&](int) { return p.flags + g0 + pp; }, 1, p.tag);
-        __syncthreads();  // every wave has seen the words: clear them
-        if (q == 0)
-            for (int pp = 0; pp < P - 1; ++pp)
-                __hip_atomic_store(p.flags + g0 + pp, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-
+        __syncthreads();
+        if (__builtin_amdgcn_readfirstlane(*counted) != P)
+            return;
+        // All parts are there: this workgroup finishes the tiles. Thread (q,
+        // lane) takes element (token 16 t + tid2 / 16, row tid2 % 16) with
+        // tid2 = 64 (q % 4) + lane of the (tile, token group) items q / 4, q / 4
+        // + 4, ...
         const int tid2 = 64 * (q & 3) + lane;
         const int mo = tid2 >> 4;  // token within its group
         const int rr = tid2 & 15;
@@ -438,8 +434,7 @@ __global__ __launch_bounds__(kSmWaves * 64) void smallm_gemm_kernel(const SmallP
         const int part_bytes = M * p.rows * 4;
         const int items = ntiles * TG;
         // (Measured and not kept: 8 items per batch, which spills the
-        // two-group kernel's registers, and the last part's own pieces kept in
-        // this XCD's L2 with plain stores and loads: 1-2 us slower each.)
+        // two-group kernel's registers: 1-2 us slower.)
         constexpr int IG = 4;  // items per thread and batch
         constexpr int PC = 4;  // parts per batch (all loads of a batch in flight before its additions)
         for (int k0 = q >> 2; k0 < items; k0 += 4 * IG) {

@@ -25,11 +25,11 @@ size_t smallm_partial_floats(int M, int K, int N);
 // fp32 floats of the dual GEMM's partial sums (0 when it needs none).
 size_t smallm_dual_partial_floats(int M, int K, int N);
 
-// 64-bit ready words that a split reduction of either GEMM uses (0 when
-// neither is split): one per workgroup, set to a per-launch tag by the
-// workgroups of the lower parts and cleared by the one that finishes their
-// tiles, so they need no initialisation; the two GEMMs of a forward may share
-// them (stream-ordered).
+// 64-bit words that a split reduction of either GEMM uses (0 when neither is
+// split): room for one per workgroup; each tile group's parts count in one,
+// under the launch's tag, and the workgroup that finishes the tiles clears it,
+// so they need no initialisation; the two GEMMs of a forward may share them
+// (stream-ordered).
 size_t smallm_flag_words(int M, int K, int N);
 
 // Dual GEMM (gate and up; out = OUT_F32_PAIR or OUT_H_*); `partials` holds

@@ -137,7 +137,7 @@ SmallParams params(int M, const void *in0, const WeightArg &w0, const WeightArg 
     p.part0 = part0;
     p.part1 = part1;
     p.flags = flags;
-    p.tag = s.parts > 1 ? launch_tag() : 0;
+    p.tag = s.parts > 1 ? tag_of_launch(launch_tag()) : 0;
     return p;
 }
 
@@ -180,7 +180,7 @@ hipError_t launch_smallm_dual(int M, OutKind out, const void *x, const WeightArg
         return hipErrorNotSupported;
     const SmallPlan s = plan(N, K, M, 2);
     // A reduction split in parts: both projections' pieces, finished by the
-    // last part's workgroup of each tile group.
+    // workgroup of each tile group that is done last.
     float *gpart = nullptr, *upart = nullptr;
     if (s.parts > 1) {
         if (partials == nullptr || flags == nullptr)
