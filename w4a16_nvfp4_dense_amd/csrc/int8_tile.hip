@@ -53,6 +53,7 @@
 #include "int8_device.h"
 #include "int8_split.h"
 #include "kernels.h"
+#include "shared_word_device.h"
 
 // Every piece of the kernel is inlined: a closure left in memory would put the
 // loop's state there.

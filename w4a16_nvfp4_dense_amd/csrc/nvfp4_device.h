@@ -111,12 +111,12 @@ __device__ __forceinline__ void wait_vmcnt()
 // with stores and loads that carry the device-scope cache policy (sc1, as
 // agent-scope atomics use): a store is written through the XCD's L2 to
 // memory, a load is not served by a line another XCD may have changed. A
-// writer counts itself in the result's word (shared_word.h), an agent-scope
-// atomic, once its own stores have completed (s_waitcnt vmcnt(0)); whoever finds
-// all parts counted there reads them. (A release fence instead writes back
-// the XCD's whole L2, which holds what the GEMMs keep resident: 21 us slower
-// per prefill forward; 8-byte atomic stores for the data, which leave half
-// lines to merge below the L2, 9 us slower.)
+// writer publishes with an agent-scope atomic store of the launch's tag to a
+// ready word once its own stores have completed (s_waitcnt vmcnt(0)); the
+// reader waits for the tag. (A release fence instead writes back the XCD's
+// whole L2, which holds what the GEMMs keep resident: 21 us slower per
+// prefill forward; 8-byte atomic stores for the data, which leave half lines
+// to merge below the L2, 9 us slower.)
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t raw_buffer(const void *base, int bytes)
 {
     // word 3: the raw-buffer format bits of gfx9 devices
@@ -138,28 +138,6 @@ __device__ __forceinline__ float load_device_coherent_f32(__amdgpu_buffer_rsrc_t
 {
     return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, byte_off, 0, 16 /* sc1 */));
 }
-
-// A word of the workspace in which workgroups on any XCD count (shared_word.h).
-struct SharedWord {
-    unsigned long long *at;
-    __device__ __forceinline__ bool exchange(unsigned long long &seen, unsigned long long next) const
-    {
-        return __hip_atomic_compare_exchange_strong(at, &seen, next, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
-                                                    __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __device__ __forceinline__ unsigned long long add_one() const
-    {
-        return __hip_atomic_fetch_add(at, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __device__ __forceinline__ unsigned long long load() const
-    {
-        return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __device__ __forceinline__ void clear() const
-    {
-        __hip_atomic_store(at, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-};
 
 // Waits (bounded: a correct launch never reaches the limit) until the n ready
 // words word(0) .. word(n - 1) all hold `tag`. A poll has the loads of up to

@@ -67,7 +67,7 @@
 
 #include "kernels.h"
 #include "nvfp4_device.h"
-#include "shared_word.h"
+#include "shared_word_device.h"
 
 namespace ffn {
 
