@@ -94,7 +94,7 @@ int ffn_w4a4_forward(const void *x, int M, int K, int N, const ffn_mxfp4_weight 
 
 /* Bytes of device workspace ffn_w4a4_down_gemm and ffn_w4a4_forward_fp4 need
  * for (M, K, N): mx(x), h [M, N] bf16, mx(h), and the down projection's fp32
- * partial sums and ready words when its reduction is split over the compute
+ * partial sums and their counts when its reduction is split over the compute
  * units (about 8 MB at K = 5120; one block of 128 token rows at a time);
  * each part rounded up to 256 bytes. 0 if M = 0 or the shape is unsupported
  * (as ffn_w4a4_dual_gemm, and N a multiple of 256). Contents need no

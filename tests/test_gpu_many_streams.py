@@ -29,6 +29,17 @@ arm("small_m40", 40, 5120, 17408)(_w4a16)       # three and six parts
 arm("small_m33_short", 33, 5376, 2048)(_w4a16)
 
 
+def _fp4(M, K, N):
+    """All three projections on 4 bits: the down product's reduction is split in parts."""
+    return (ffn.w4a4_fp4_workspace_bytes(M, K, N), lambda w: [ffn.w4a4_prepare_weight(v) for v in w],
+            ffn.w4a4_forward_fp4)
+
+
+arm("fp4_m128", 128, 5120, 17408)(_fp4)
+arm("fp4_m40_eight_parts", 40, 1024, 4096)(_fp4)
+arm("fp4_m200", 200, 2048, 4096)(_fp4)  # two launches on the same words
+
+
 @pytest.fixture(scope="module", params=list(ARMS))
 def case(request):
     M, K, N, make = ARMS[request.param]

@@ -1,5 +1,6 @@
-"""No kernel waits for another workgroup (host only: read from the sources). One that waits holds a compute unit that
-the one it waits for may need while other launches hold the rest."""
+"""No kernel's result rests on a wait for another workgroup (host only: read from the sources). One that waits holds a
+compute unit that the one it waits for may need while other launches hold the rest; a wait that gives up and goes on
+all the same gives wrong results. Looking a bounded time, with a way to finish whatever is found, is neither."""
 import os
 
 import pytest
@@ -9,7 +10,7 @@ import w4a16_nvfp4_dense_amd as ffn
 CSRC = os.path.join(ffn.PKG_DIR, "csrc")
 
 
-@pytest.mark.parametrize("name", ["smallm_gemm.h"])
+@pytest.mark.parametrize("name", ["smallm_gemm.h", "w4a4.hip"])
 def test_no_wait(name):
     with open(os.path.join(CSRC, name)) as f:
         text = f.read()

@@ -61,7 +61,7 @@ W4Layout layout(int M, int K, int N)
 }
 
 // Workspace of the all-FP4 entries: [mx(x) codes][mx(x) exponents][h]
-// [mx(h) codes][mx(h) exponents][down partial sums][ready words] (the down
+// [mx(h) codes][mx(h) exponents][down partial sums][their counts] (the down
 // entry uses the parts from mx(h) on).
 struct Fp4Layout {
     size_t xe, h, hc, he, part, flags, total;
@@ -100,7 +100,7 @@ int launch_status(hipError_t e)
 
 // h [M, N] bf16 -> MXFP4 in the workspace, then the down GEMM in blocks of
 // 128 token rows (one launch each; the blocks share the partial sums and
-// ready words, in stream order).
+// counts, in stream order).
 hipError_t run_fp4_down(const void *h, int M, int K, int N, const ffn_mxfp4_weight *down, uint8_t *ws,
                         const Fp4Layout &l, void *out, hipStream_t stream)
 {
