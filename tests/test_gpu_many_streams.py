@@ -29,6 +29,12 @@ arm("small_m40", 40, 5120, 17408)(_w4a16)       # three and six parts
 arm("small_m33_short", 33, 5376, 2048)(_w4a16)
 
 
+arm("prefill_m64", 64, 5120, 17408)(_w4a16)     # 128-row arm: the dual product finishes its split tiles in the launch
+arm("prefill_m128", 128, 5120, 17408)(_w4a16)
+arm("prefill_m41_short", 41, 2048, 1088)(_w4a16)   # many pieces of a tile
+arm("prefill_m200", 200, 1024, 8256)(_w4a16)    # two blocks on the same words
+
+
 def _fp4(M, K, N):
     """All three projections on 4 bits: the down product's reduction is split in parts."""
     return (ffn.w4a4_fp4_workspace_bytes(M, K, N), lambda w: [ffn.w4a4_prepare_weight(v) for v in w],

@@ -10,7 +10,7 @@ import w4a16_nvfp4_dense_amd as ffn
 CSRC = os.path.join(ffn.PKG_DIR, "csrc")
 
 
-@pytest.mark.parametrize("name", ["smallm_gemm.h", "w4a4.hip"])
+@pytest.mark.parametrize("name", ["smallm_gemm.h", "w4a4.hip", "mfma_gemm.h"])
 def test_no_wait(name):
     with open(os.path.join(CSRC, name)) as f:
         text = f.read()

@@ -51,18 +51,19 @@
 //    its piece of a shared tile (the top of its range) first and the highest
 //    one (whose range starts inside the tile) reaches it last. The lower ones
 //    store their pieces with device-coherent 16-byte stores (sc1: written
-//    through to memory, past the XCD's L2) and then set one ready word per
-//    wave to the launch's tag; the highest waits for those words, reads the
-//    pieces with device-coherent loads, adds them nearest first and runs the
-//    epilogue. A workgroup only ever waits for lower-numbered ones, which
-//    were dispatched first and wait only for lower ones still, so the waits
-//    end even when not all workgroups are resident at once. No fence is
-//    used: a release fence writes back the XCD's whole L2, which holds the
-//    activation block.
+//    through to memory, past the XCD's L2) and then mark one word per wave;
+//    the highest, finding them marked, reads the pieces with device-coherent
+//    loads, adds them nearest first and runs the epilogue. It waits for them a
+//    bounded time; whatever is late then, some wave finishes its part of the
+//    tile, in the same order (part_words.h): workgroups that waited for others
+//    without a bound would hold compute units that those may need, where
+//    launches on other streams hold the rest. No fence is used: a release
+//    fence writes back the XCD's whole L2, which holds the activation block.
 #pragma once
 
 #include "kernels.h"
 #include "nvfp4_device.h"
+#include "part_words_device.h"
 
 namespace ffn {
 
@@ -83,8 +84,8 @@ struct MfmaParams {
     void *out0;
     void *out1;
     float *partials;   // 2 G slots of partial tiles (stream-K only)
-    unsigned long long *flags;  // 4 ready words per slot (in-kernel finishing only)
-    unsigned long long tag;     // this launch's ready value (nonzero)
+    unsigned long long *flags;  // 4 words per slot (in-kernel finishing only)
+    unsigned long long tag;     // this launch's tag for them
     int M;             // token rows, 1 <= M <= 32 * MT
     int rows;          // weight rows (output columns)
     int cols;          // reduction length, a multiple of 64
@@ -382,16 +383,46 @@ __global__ __launch_bounds__(kMfmaWaves * 64) void mfma_gemm_kernel(const MfmaPa
         // tokens with the 4-stage ring.)
     };
 
-    // FIX: finish tile t, whose top unit this workgroup's current piece
-    // holds (acc): add the lower workgroups' pieces of the tile to it, the
-    // nearest first (a fixed order: a tile's sum depends only on the shape),
-    // each piece's loads all in flight before its additions.
-    auto finish = [&](int t) {
-        const int g_lo = sk_owner(static_cast<long long>(t) * KU, U, G);
-        for (int gg = g - 1; gg >= g_lo; --gg) {
-            unsigned long long *flag = p.flags + 4 * (2 * gg + (t == sk_begin(gg, U, G) / KU ? 0 : 1)) + wave;
-            wait_ready([&](int) { return flag; }, 1, p.tag);
-            __hip_atomic_store(flag, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // FIX: this wave's part of a piece to its slot, for another compute unit to
+    // read in this launch.
+    auto store_piece = [&](int t) {
+        const __amdgpu_buffer_rsrc_t rsrc = raw_buffer(slot_ptr(g, t), SLOT / kMfmaWaves * 4);
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    const f32x4_t v = {acc[f][mt][4 * q4], acc[f][mt][4 * q4 + 1], acc[f][mt][4 * q4 + 2],
+                                       acc[f][mt][4 * q4 + 3]};
+                    store_device_coherent(rsrc, (((f * MT + mt) * 4 + q4) * 64 + opaque_lane(lane)) * 16, v);
+                }
+    };
+    // FIX: a wave's word for the lower piece of a tile that workgroup gg holds (one
+    // at most), and for the top piece (one at most).
+    auto lower_word = [&](int gg) { return PartWord{p.flags + 8 * gg + wave}; };
+    auto top_word = [&](int gg) { return PartWord{p.flags + 8 * gg + 4 + wave}; };
+    // FIX: finish tile t of workgroups g_lo .. g_hi: to the highest one's piece
+    // (acc, where this workgroup holds it) add the lower ones', the nearest first
+    // (a fixed order: a tile's sum depends only on the shape), each piece's
+    // loads all in flight before its additions.
+    auto finish = [&](int t, int g_lo, int g_hi) {
+        if (g != g_hi) {
+            const __amdgpu_buffer_rsrc_t rsrc = raw_buffer(slot_ptr(g_hi, t), SLOT / kMfmaWaves * 4);
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const f32x4_t v = load_device_coherent(
+                            rsrc, (((f * MT + mt) * 4 + q4) * 64 + opaque_lane(lane)) * 16);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            acc[f][mt][4 * q4 + c] = v[c];
+                    }
+        }
+        for (int gg = g_hi - 1; gg >= g_lo; --gg) {
             const __amdgpu_buffer_rsrc_t rsrc = raw_buffer(slot_ptr(gg, t), SLOT / kMfmaWaves * 4);
             f32x4_t v[2][MT][4];
 #pragma unroll
@@ -412,14 +443,32 @@ __global__ __launch_bounds__(kMfmaWaves * 64) void mfma_gemm_kernel(const MfmaPa
                         for (int c = 0; c < 4; ++c)
                             acc[f][mt][4 * q4 + c] += v[f][mt][q4][c];
         }
+        for (int gg = g_lo + lane; gg < g_hi; gg += 64)
+            lower_word(gg).clear();
+        if (lane == 0)
+            top_word(g_hi).clear();
         store_out(t);
+    };
+    // FIX: the first lane's finding, for the wave.
+    auto one_finds = [&](auto find) {
+        int found = 0;
+        if (lane == 0)
+            found = find();
+        return __builtin_amdgcn_readfirstlane(found) != 0;
+    };
+    // (divisions run on the vector unit; the results go back to scalar registers)
+    auto lowest = [&](int t) {
+        return __builtin_amdgcn_readfirstlane(sk_owner(static_cast<long long>(t) * KU, U, G));
+    };
+    auto highest = [&](int t) {
+        return __builtin_amdgcn_readfirstlane(sk_owner(static_cast<long long>(t) * KU + KU - 1, U, G));
     };
 
     // Pieces: maximal runs of this workgroup's units inside one tile. The
     // ring runs on across pieces; the accumulators only live inside one.
     int j = 0;
-    int fin_t = -1;       // FIX: the tile this workgroup finishes after its loop
-    int wrote = 0;        // FIX: slots it wrote (bit 0: slot 2 g, bit 1: 2 g + 1), published at the end
+    int fin_t = -1;       // FIX: the tile whose top piece this workgroup holds after its loop
+    int low_t = -1;       // FIX: the tile (one at most) of which it stored a lower piece, marked at the end
     while (j < n) {
         int t, ku0, len;
         if constexpr (FIX) {
@@ -458,7 +507,7 @@ __global__ __launch_bounds__(kMfmaWaves * 64) void mfma_gemm_kernel(const MfmaPa
             // A piece that holds its tile's top unit without being the whole
             // tile starts inside the tile, so at the range's first unit: in
             // decreasing order it is the workgroup's last piece. The tile is
-            // finished after the ready words of this workgroup are set.
+            // finished after this workgroup's own lower piece is marked.
             if (ku0 + len == KU) {
                 fin_t = t;
                 break;
@@ -466,41 +515,60 @@ __global__ __launch_bounds__(kMfmaWaves * 64) void mfma_gemm_kernel(const MfmaPa
         }
         // A piece of a tile shared with other workgroups: to its slot, for
         // mfma_reduce_kernel or (FIX) the workgroup that finishes the tile.
-        float *part = slot_ptr(g, t);
-        f32x4_t *mine = reinterpret_cast<f32x4_t *>(part) + opaque_lane(lane);
-        const __amdgpu_buffer_rsrc_t rsrc = raw_buffer(part, SLOT / kMfmaWaves * 4);
+        if constexpr (FIX) {
+            store_piece(t);
+            low_t = t;
+        } else {
+            f32x4_t *mine = reinterpret_cast<f32x4_t *>(slot_ptr(g, t)) + opaque_lane(lane);
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+            for (int f = 0; f < 2; ++f)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    const f32x4_t v = {acc[f][mt][4 * q4], acc[f][mt][4 * q4 + 1], acc[f][mt][4 * q4 + 2],
-                                       acc[f][mt][4 * q4 + 3]};
-                    const int idx = ((f * MT + mt) * 4 + q4) * 64;
-                    if constexpr (FIX)  // read by another compute unit in this launch
-                        store_device_coherent(rsrc, (idx + opaque_lane(lane)) * 16, v);
-                    else
-                        mine[idx] = v;
-                }
-        if constexpr (FIX)
-            wrote |= (t == sk_begin(g, U, G) / KU) ? 1 : 2;
+                    for (int q4 = 0; q4 < 4; ++q4)
+                        mine[((f * MT + mt) * 4 + q4) * 64] = f32x4_t{acc[f][mt][4 * q4], acc[f][mt][4 * q4 + 1],
+                                                                     acc[f][mt][4 * q4 + 2], acc[f][mt][4 * q4 + 3]};
+        }
     }
     if constexpr (FIX) {
-        // Publish this wave's part of the slot written above once its
-        // device-coherent stores have completed (nothing else is in flight at
-        // the end of the range). (A release fence instead, which writes the
-        // XCD's L2 back, measured 21 us slower per forward.)
-        if (wrote != 0) {
+        // Mark this wave's part of the lower piece once its device-coherent
+        // stores have completed (nothing else is in flight at the end of the
+        // range). (A release fence instead, which writes the XCD's L2 back,
+        // measured 21 us slower per forward.)
+        unsigned long long was = 0;  // (used only after the top piece is dealt with)
+        if (low_t >= 0) {
             wait_vmcnt<0>();
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                if (wrote & (1 << b))
-                    __hip_atomic_store(p.flags + 4 * (2 * g + b) + wave, p.tag, __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
+            if (lane == 0)
+                was = lower_word(g).swap(marked(p.tag));
         }
-        if (fin_t >= 0)
-            finish(fin_t);
+        if (fin_t >= 0) {
+            const int g_lo = lowest(fin_t), parts = g - g_lo + 1;
+            bool mine = true;
+            for (int gg = g - 1; gg >= g_lo && mine; --gg)
+                mine = comes(lower_word(gg), p.tag);
+            if (!mine) {
+                store_piece(fin_t);
+                wait_vmcnt<0>();
+                mine = one_finds([&]() {
+                    return last_gives_up([&](int i) { return lower_word(g_lo + i); }, top_word(g), p.tag, parts);
+                });
+            }
+            if (!mine)
+                fin_t = -1;
+        }
+        if (low_t >= 0) {
+            const bool late = one_finds([&]() { return was == given_up(p.tag); });
+            if (!late || !one_finds([&]() {
+                    const int g_hi = highest(low_t);
+                    return late_part(top_word(g_hi), p.tag, g_hi - lowest(low_t) + 1);
+                }))
+                low_t = -1;
+        }
+        while (fin_t >= 0 || low_t >= 0) {  // (acc holds fin_t's top piece)
+            int &next = fin_t >= 0 ? fin_t : low_t;
+            finish(next, lowest(next), highest(next));
+            next = -1;
+        }
     }
 }
 

@@ -12,8 +12,9 @@ constexpr int kMfmaMaxM = 128;     // token rows per launch (larger batches are 
 constexpr int kMfmaMaxGrid = 256;  // workgroups of a stream-K launch
 
 // Stream-K scratch: the partial-tile slots and, for the dual GEMM's in-kernel
-// finishing, one 64-bit ready word per slot and wave (set to a per-launch tag
-// by the writer, cleared by the reader; contents need no initialisation).
+// finishing, one 64-bit word per slot and wave (part_words.h: marked with the
+// launch's tag by the writer, cleared by the reader; contents need no
+// initialisation).
 struct MfmaScratch {
     float *partials;             // mfma_partials_floats() floats
     unsigned long long *flags;   // mfma_flag_words() words

@@ -37,9 +37,9 @@ hipError_t launch_t(MfmaParams p, int G, hipStream_t stream)
 }
 
 // The GEMM, then (stream-K) the reduction of the split tiles. The dual GEMM
-// finishes its split tiles in the kernel when the scratch has ready words:
+// finishes its split tiles in the kernel when the scratch has words for them:
 // the workgroup holding a tile's last unit adds the lower workgroups' pieces
-// once their ready words carry this launch's tag.
+// once their words are marked.
 template <int MT, int NMAT, int IN, int OUT>
 hipError_t launch_gemm_reduce(const MfmaParams &p, int G, hipStream_t stream)
 {
@@ -86,7 +86,7 @@ void plan(MfmaParams &p, int nmat, const MfmaScratch *ws, int &G)
         return;  // every workgroup owns whole tiles
     p.partials = ws->partials;
     p.flags = ws->flags;
-    p.tag = launch_tag();
+    p.tag = tag_of_launch(launch_tag());
 }
 
 MfmaParams params(int M, const void *in0, const float *in1, const WeightArg &w0, const WeightArg &w1, void *out0,
