@@ -15,3 +15,12 @@ def test_no_wait(name):
     with open(os.path.join(CSRC, name)) as f:
         text = f.read()
     assert "wait_ready" not in text and "s_sleep" not in text
+
+
+def test_nothing_to_wait_with():
+    """The one loop that sleeps looks a bounded number of times and returns what it found."""
+    for name in sorted(os.listdir(CSRC)):
+        with open(os.path.join(CSRC, name)) as f:
+            text = f.read()
+        assert "wait_ready" not in text, name
+        assert text.count("s_sleep") == (1 if name == "part_words_device.h" else 0), name

@@ -74,10 +74,10 @@ hipError_t launch_wave_down(int M, InKind in, const void *in0, const float *in1,
 // Number of compute units of the current device (cached per device).
 int device_cu_count();
 
-// A nonzero 64-bit tag per launch for the ready words of in-kernel exchanges
-// (a counter and this library's address through a 64-bit mix), so that a
-// ready word left in a reused workspace by other data or another launch
-// almost never equals it.
+// A nonzero 64-bit number per launch (a counter and this library's address
+// through a 64-bit mix). Its high 48 bits are the launch's tag in the words of
+// in-kernel exchanges (shared_word.h), so that a word left in a reused
+// workspace by other data or another launch almost never carries it.
 unsigned long long launch_tag();
 
 // Lanes that share one weight row for a reduction of `cpr` 32-column chunks
