@@ -7,8 +7,8 @@
 // tile may be shared by neighbouring workgroups, each with one part of its
 // stages. A workgroup walks its share downwards.
 //
-// No workgroup ever waits for another: a shared tile is finished by the one that
-// counts itself last in the tile's word (shared_word.h).
+// A shared tile is finished by its last workgroup, or whichever is late
+// (part_words.h).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -17,7 +17,7 @@
 
 #include <algorithm>
 
-#include "shared_word.h"
+#include "part_words.h"
 
 namespace ffn {
 
@@ -58,7 +58,7 @@ struct Split {
     Divisor by_stages, by_band, by_rows, by_last_rows;  // tiles of a band; its tiles of tokens, and the last one's
     unsigned long long tag;     // of this launch, its low kCountBits zero
     int32_t *part;              // two slots of a tile's sums for each sharer
-    unsigned long long *words;  // a word for each shared tile
+    unsigned long long *words;  // a word for each slot
 
     // Workgroup b's place in a round of whole tiles: those of one XCD (b % 8)
     // take neighbouring tiles, which share operands in its L2.
@@ -94,10 +94,10 @@ __host__ __device__ __forceinline__ Sharers sharers_of(const Split &s, int t)
     return Sharers{owner(s, t * s.stages), owner(s, (t + 1) * s.stages - 1)};
 }
 
-// The slot of workgroup w's sums of a tile that it shares with others. A share
-// has at most one part that stops short of its tile's last stage and one that
-// has that stage without the tile's first: the tile's last workgroup writes to
-// its second slot, every other one to its first.
+// The slot of workgroup w's sums of a tile that it shares with others, and the
+// number of its word. A share has at most one part that stops short of its
+// tile's last stage and one that has that stage without the tile's first: the
+// tile's last workgroup takes its second slot, every other one its first.
 __host__ __device__ __forceinline__ int slot_number(const Split &s, const Sharers &t, int w)
 {
     return w == t.last ? s.sharers + w : w;
@@ -194,7 +194,7 @@ inline Plan int8_plan(int M, int K, int N, int BM, int BN, int BC, int cus)
         s.least = s.shared * s.stages / s.sharers;
         s.more = s.shared * s.stages % s.sharers;
         p.part_bytes = round256(2 * static_cast<size_t>(s.sharers) * BM * BN * 4);
-        p.word_bytes = round256(static_cast<size_t>(s.shared) * 8);
+        p.word_bytes = round256(2 * static_cast<size_t>(s.sharers) * 8);
     }
     return p;
 }

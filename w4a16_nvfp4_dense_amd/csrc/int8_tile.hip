@@ -33,13 +33,13 @@
 // Work split (int8_split.h). Every workgroup takes whole tiles and then an equal
 // share of the units of the tiles that are left, walked downwards: the tile that
 // its share ends in the middle of comes first, the one that its share begins in
-// the middle of last. A workgroup with a part of a tile writes its sums to the
-// workspace and counts itself in the tile's word; the one that finds the others
-// counted adds their sums and stores the tile. The tile's last workgroup, which
-// reaches it last in its walk, looks first, and keeps its sums to itself where
-// it is the one (most tiles of two parts). Nothing ever waits for another
-// workgroup, so launches beside each other cannot hold each other up, and
-// int32 sums give the same bits whoever adds them.
+// the middle of last. The tile's last workgroup, which reaches it last in its
+// walk, adds the sums that the others have written to the workspace to its own
+// and stores the tile. It looks for them a bounded time; whatever is late then,
+// some workgroup finishes the tile (part_words.h), so launches beside each other
+// cannot hold each other up, and int32 sums give the same bits whoever adds
+// them. (Every workgroup writing its sums, and the last one counted adding them:
+// 1-2% slower at M <= 64; 44.2 us for 40.9 at M = 256, K = 5120, N = 17408.)
 //
 // A single token's real row (`row`, what is between the two products of a
 // decoded token) is quantised by every workgroup for itself before its first
@@ -53,7 +53,7 @@
 #include "int8_device.h"
 #include "int8_split.h"
 #include "kernels.h"
-#include "shared_word_device.h"
+#include "part_words_device.h"
 
 // Every piece of the kernel is inlined: a closure left in memory would put the
 // loop's state there.
@@ -296,13 +296,16 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
         wait_vmcnt<0>();
         lds_barrier();  // every wave's stores have completed
     };
-    // What thread 0 says, to every thread. (16 bytes behind the ring and a
-    // row's codes; two uses have a barrier between them.)
+    // What the first wave finds, to every thread. (16 bytes behind the ring and
+    // a row's codes; two uses have a barrier between them.)
     const int note_at = STAGES * STAGE + (ROW ? sp.stages * kBk : 0);
-    const auto agree = [&](auto decide) FFN_INLINE {
+    const auto agree = [&](auto find) FFN_INLINE {
         int *note = reinterpret_cast<int *>(lds + note_at);
-        if (threadIdx.x == 0)
-            *note = decide() ? 1 : 0;
+        if (wave == 0) {
+            const bool found = find();
+            if (lane == 0)
+                *note = found;
+        }
         lds_barrier();
         return __builtin_amdgcn_readfirstlane(*note) != 0;
     };
@@ -310,24 +313,23 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
     // tile: then the others' sums are in their slots.
     const auto take = [&](int tile, const Sharers &in) FFN_INLINE {
         const int parts = in.last - in.first + 1;
-        const SharedWord word{sp.words + (tile - sp.whole * G)};
-        unsigned long long seen = 0;
-        if (b == in.last)
-            if (agree([&]() FFN_INLINE {
-                    seen = word.load();
-                    const bool all = seen == sp.tag + (parts - 1);
-                    if (all)
-                        word.clear();
-                    return all;
-                }))
-                return true;
-        publish(tile, slot_number(sp, in, b));
-        return agree([&]() FFN_INLINE {
-            const bool all = count_part(word, sp.tag, seen) == parts;
-            if (all)
-                word.clear();
-            return all;
-        });
+        const auto word = [&](int i) FFN_INLINE {
+            return PartWord{sp.words + slot_number(sp, in, in.first + i)};
+        };
+        bool mine = b == in.last && agree([&]() FFN_INLINE { return all_come(word, parts - 1, sp.tag); });
+        if (!mine) {
+            publish(tile, slot_number(sp, in, b));
+            mine = agree([&]() FFN_INLINE {
+                if (lane != 0)
+                    return false;
+                return b == in.last ? last_gives_up(word, word(parts - 1), sp.tag, parts)
+                                    : word(b - in.first).swap(marked(sp.tag)) == given_up(sp.tag) &&
+                                          late_part(word(parts - 1), sp.tag, parts);
+            });
+        }
+        if (mine && threadIdx.x < parts)
+            word(threadIdx.x).clear();
+        return mine;
     };
     // The scales of a tile, for this lane's FC channels and GROUPS groups of
     // four tokens. Small tiles read them when a tile begins, so that they are

@@ -543,15 +543,12 @@ __global__ __launch_bounds__(kMfmaWaves * 64) void mfma_gemm_kernel(const MfmaPa
         }
         if (fin_t >= 0) {
             const int g_lo = lowest(fin_t), parts = g - g_lo + 1;
-            bool mine = true;
-            for (int gg = g - 1; gg >= g_lo && mine; --gg)
-                mine = comes(lower_word(gg), p.tag);
+            auto lower = [&](int i) { return lower_word(g_lo + i); };
+            bool mine = all_come(lower, parts - 1, p.tag);
             if (!mine) {
                 store_piece(fin_t);
                 wait_vmcnt<0>();
-                mine = one_finds([&]() {
-                    return last_gives_up([&](int i) { return lower_word(g_lo + i); }, top_word(g), p.tag, parts);
-                });
+                mine = one_finds([&]() { return last_gives_up(lower, top_word(g), p.tag, parts); });
             }
             if (!mine)
                 fin_t = -1;

@@ -20,12 +20,18 @@ struct PartWord : SharedWord {
     }
 };
 
-// Whether a lower part's word comes to be marked within the last part's time (the
-// same answer in every active lane of a wave).
-__device__ __forceinline__ bool comes(const PartWord &word, unsigned long long tag)
+// Whether the words of the first n parts, lower(i), come to be marked within the
+// last part's time. A wave looks at 64 of them together; every lane of it calls
+// this, and has the same answer.
+template <class LowerWord>
+__device__ __forceinline__ bool all_come(LowerWord lower, int n, unsigned long long tag)
 {
+    const int lane = threadIdx.x & 63;
     for (int i = 0; i < kLooks; ++i) {
-        if (__builtin_amdgcn_readfirstlane(word.load() == marked(tag)))
+        bool there = true;
+        for (int k = lane; k < n; k += 64)
+            there = there && lower(k).load() == marked(tag);
+        if (__all(there))
             return true;
         __builtin_amdgcn_s_sleep(1);
     }

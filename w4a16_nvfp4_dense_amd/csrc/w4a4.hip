@@ -389,15 +389,14 @@ __global__ __launch_bounds__(kW4Threads) void w4a4_gemm_kernel(const W4a4Params 
             const int part_bytes = p.M * p.N * 4;  // <= 128 x 65536 x 4
             const int g0 = static_cast<int>(blockIdx.x) - part;
             const auto word = [&](int i) { return PartWord{p.flags + g0 + i}; };
-            FFN_LDS int *note = (FFN_LDS int *)lds;  // what thread 0 finds
+            FFN_LDS int *note = (FFN_LDS int *)lds;  // what the first wave finds
             bool mine = false;                       // whether this workgroup finishes the block
             if (part == P - 1) {
                 __syncthreads();  // every wave is done with the ring
-                if (threadIdx.x == 0) {
-                    bool there = true;
-                    for (int i = 0; i < P - 1 && there; ++i)
-                        there = comes(word(i), p.tag);
-                    *note = there;
+                if (wave == 0) {
+                    const bool there = all_come(word, P - 1, p.tag);
+                    if (lane == 0)
+                        *note = there;
                 }
                 __syncthreads();
                 mine = __builtin_amdgcn_readfirstlane(*note);
