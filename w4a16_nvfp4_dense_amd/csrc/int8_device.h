@@ -84,7 +84,9 @@ __device__ __forceinline__ float int8_biased(float v, float b)
 }
 
 // act(g) * u in fp32, both gates as g / (1 + e^z): z = -g for SiLU and
-// z = -2 sqrt(2/pi) (g + 0.044715 g^3) for GELU-tanh.
+// z = -2 sqrt(2/pi) (g + 0.044715 g^3) for GELU-tanh. (gate_act's formulas, again
+// because that leaves it to the compiler where a product and a sum are fused:
+// here every tile shape has to round alike.)
 template <int OUT>
 __device__ __forceinline__ float int8_gated(float g, float u)
 {

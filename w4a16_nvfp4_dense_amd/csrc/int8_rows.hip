@@ -17,11 +17,11 @@
 //
 // What bounds it, measured on one MI355X: memory for many rows, and for few the
 // launch and the two reductions' latency.
-//   norm with residual, bf16, 8192 x 5120   52.2 us, 294 MB: 5.6 TB/s (47.4
+//   norm with residual, bf16, 8192 x 5120   52.4 us, 294 MB: 5.6 TB/s (47.4
 //                                           where x was written just before)
-//   the same, 1 x 5120                       3.4 us
+//   the same, 1 x 5120                       3.6 us
 //   norm with residual, fp32, 333 x 5376     7.9 us, 23 MB
-//   bf16 rows, 17408 x 5120                 44.7 us, 267 MB: 6.0 TB/s
+//   bf16 rows, 17408 x 5120                 45.0 us, 267 MB: 6.0 TB/s
 //   fp16 rows, 3 x 17408                     3.2 us
 //   fp32 rows, 2048 x 17408, just written   27.1 us, 178 MB: 6.6 TB/s
 //   NVFP4 rows, 17408 x 5120                44.6 us, 139 MB, two thirds of them

@@ -180,8 +180,8 @@ inline Plan int8_plan(int M, int K, int N, int BM, int BN, int BC, int cus)
     // At least four units to a share; and after whole rounds shares of half a
     // tile or more, so that a tile has two parts, or three where the shares'
     // ends drift off the tiles' middles (an odd number of stages, or more
-    // left-over tiles than half the workgroups). (5120/17408, M = 4096: 372 us;
-    // four parts 387-408.)
+    // left-over tiles than half the workgroups). (5120/17408, M = 4096: 387 us;
+    // four parts 393, whole tiles 389.)
     const long units = static_cast<long>(s.shared) * s.stages;
     s.sharers = static_cast<int>(std::min<long>(s.whole > 0 ? std::min(p.groups, 2 * s.shared) : p.groups,
                                                 std::max<long>(1, units / 4)));

@@ -11,16 +11,17 @@
 // 2450 - 2640 TOPS. In short runs at 2.1 GHz the matrix cores are busy 57% of the
 // time, and LDS reads and writes take as many cycles as the products. Measured
 // on one MI355X, weights not in a cache at M <= 128 (K/N; "dual" with h):
-//   M = 1     dual 5120/17408  32.5 us, 178 MB: 5.5 TB/s
-//             17408/5120, h quantised here too  19.0 - 21.6 us, 89 MB: 4.1 -
-//             4.7 TB/s; 5120/17408 18.2 us
-//   M = 32    dual 5376/21504  46.7 us, 231 MB: 5.0 TB/s
-//             21504/5376       27.3 us, 116 MB: 4.3 TB/s
-//   M = 128   dual 5120/17408  54.0 us, 845 TOPS; 17408/5120 33.6 us
+//   M = 1     dual 5120/17408  32.2 - 32.6 us, 178 MB: 5.5 TB/s
+//             17408/5120, h quantised here too  19.5 - 21.8 us, 89 MB: 4.1 -
+//             4.6 TB/s; 5120/17408 18.0 us
+//   M = 32    dual 5376/21504  46.4 - 47.2 us, 231 MB: 5.0 TB/s
+//             21504/5376       27.0 us, 116 MB: 4.3 TB/s
+//   M = 128   dual 5120/17408  53.0 - 53.9 us, 860 TOPS; 17408/5120 33.2 us
 //   M = 300   4112/4099 fp32   21.2 us, 478 TOPS
-//   M = 2048  dual 5120/17408  380 us, 1920 TOPS; 17408/5120 194 us, 1880 TOPS
-//   M = 4096  5120/17408       330 - 351 us, 2080 - 2210 TOPS (4 waves of
-//             128 x 128 instead of 8 of 64 x 128, which read LDS less: 359)
+//   M = 2048  dual 5120/17408  369 - 388 us, 1880 - 1980 TOPS; 17408/5120
+//             184 - 193 us, 1890 - 1980 TOPS
+//   M = 4096  5120/17408       346 us, 2110 TOPS (4 waves of 128 x 128 instead
+//             of 8 of 64 x 128, which read LDS less: 8% slower)
 //
 // Layout. A stage holds 128 columns of BM token rows and BN weight rows, 128
 // bytes a row, written by direct global -> LDS loads of 16 bytes a lane (eight
@@ -520,8 +521,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void int8_tile_kernel(Int8GemmArgs 
     int spare = total - (STAGES - 1);  // units past those the ring holds now
     // To the next unit, every wave being done with the one before: it has
     // landed once at most the STAGES - 2 later ones' loads are in flight (loads
-    // return in order; a last stage through registers has waited for
-    // everything before it). Its predecessor's slot takes the next load.
+    // return in order). Its predecessor's slot takes the next load.
     const auto enter = [&]() FFN_INLINE {
         if (spare < 0)
             wait_vmcnt<0>();
@@ -642,8 +642,8 @@ hipError_t launch_t(const Int8GemmArgs &a, void *workspace, size_t *need, hipStr
 
 // Weights of this size are read non-temporally where every byte is read once:
 // with those of the layer before them they do not stay in the 256 MB
-// last-level cache anyway. (178 MB at M = 1: 34.7 us for 38.1 with other
-// weights in between, but 33.6 for 31.4 if the same ones are read again and
+// last-level cache anyway. (178 MB at M = 1: 32.0 us for 35.4 with other
+// weights in between, but 30.6 for 29.0 if the same ones are read again and
 // again; 89 MB: no difference.)
 constexpr size_t kStreamBytes = size_t{128} << 20;
 
@@ -651,19 +651,19 @@ constexpr size_t kStreamBytes = size_t{128} << 20;
 // on one MI355X, K/N as given, G the dual of K = 5120 and N = 17408):
 //   M <= 16, 32     the smallest that hold the tokens, 128 weight rows; 64 rows
 //                   where 128 at a time leave half the compute units without a
-//                   tile (17408/5120: M = 1 20.8 us for 22.2, M = 32 22.0 for
-//                   23.9; 21504/5376: no difference)
-//   M <= 64         64 x 128 (G, M = 64: 47.1 us; 64 x 64: 48.6), 64 x 64
+//                   tile (17408/5120: M = 1 19.4 us for 20.8, M = 32 19.8 for
+//                   22.0; 21504/5376, M = 32: 26.1 for 27.0)
+//   M <= 64         64 x 128 (G, M = 64: 46.3 us; 64 x 64: 48.6), 64 x 64
 //                   where 128 channels at a time leave half the compute units
-//                   without a tile (17408/5120: 24.6 us for 26.7)
+//                   without a tile (17408/5120: 23.1 us for 24.6)
 //   M <= 128, and more tokens that fill tiles of 256 badly: 128 x 128 (G,
-//                   M = 128: 54.0 us; 128 x 64: 65.9), 128 x 64 by the same
-//                   rule (17408/5120: 31.5 us for 35.2; M = 300, 4112/4099:
-//                   22.2 for 23.8)
+//                   M = 128: 53.9 us; 128 x 64: 65.9), 128 x 64 by the same
+//                   rule (17408/5120: 29.8 us for 33.1; M = 300, 4112/4099:
+//                   21.1 for 21.4)
 //   more            256 x 256 from 0.6 tiles a compute unit on (5120/17408,
-//                   M = 4096: 373 us; 256 x 128: 401; 128 x 128: 528),
+//                   M = 4096, traced: 387 us; 256 x 128: 431; 128 x 128: 484),
 //                   256 x 128 from half a tile a compute unit on (G, M = 256:
-//                   65.8 us; 128 x 128: 90.5)
+//                   72.5 us; 128 x 128: 88.4)
 template <int OUT>
 hipError_t launch_out(const Int8GemmArgs &a, void *workspace, size_t *need, hipStream_t stream)
 {
