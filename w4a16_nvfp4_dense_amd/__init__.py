@@ -48,6 +48,14 @@ and the int8 (W8A8) arm with the operators around it (``include/ffn_int8.h``):
 * :func:`int8_dual_gemm` -- ``ffn_int8_dual_gemm`` act(gate) * up -> int8 codes, scales
 * :func:`int8_forward`   -- ``ffn_int8_forward`` the whole FFN
 * :func:`int8_gemm_workspace_bytes`, :func:`int8_workspace_bytes`
+
+and the sparse (mixture of experts) FFN over NVFP4 experts (``include/ffn_moe.h``):
+
+* :func:`moe_route`   -- ``ffn_moe_route`` the top_k experts of each token and their weights
+* :func:`moe_plan`    -- ``ffn_moe_plan`` expert order of the chosen (token, expert) pairs
+* :func:`moe_gemm`    -- ``ffn_moe_gemm`` the product grouped by expert, ragged sizes
+* :func:`moe_forward` -- ``ffn_moe_forward`` the whole sparse FFN
+* :func:`moe_plan_workspace_bytes`, :func:`moe_workspace_bytes`
 """
 from __future__ import annotations
 
@@ -62,10 +70,14 @@ HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_nvfp4.h")
 FP8_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_fp8.h")
 W4A4_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_w4a4.h")
 INT8_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_int8.h")
+MOE_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_moe.h")
 DIAG_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "ffn_diag.h")
 
 ACT_SILU = 0
 ACT_GELU_TANH = 1
+
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
 
 OK = 0
 ERR_NULL = -1
@@ -109,6 +121,12 @@ class Int8WeightStruct(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class MoeWeightStruct(ctypes.Structure):
+    """ffn_moe_weight: device codes, scales and fp32 scale2 of E experts."""
+
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("scale2", ctypes.c_void_p)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _P = ctypes.c_void_p
@@ -117,6 +135,7 @@ _WP = ctypes.POINTER(WeightStruct)
 _FP = ctypes.POINTER(Fp8WeightStruct)
 _MP = ctypes.POINTER(MxWeightStruct)
 _QP = ctypes.POINTER(Int8WeightStruct)
+_EP = ctypes.POINTER(MoeWeightStruct)
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -186,6 +205,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ffn_int8_dual_gemm.argtypes = [_P, _P, _I, _I, _I, _QP, _QP, _I, _P, _P, _P, ctypes.c_size_t, _P]
     lib.ffn_int8_forward.restype = _I
     lib.ffn_int8_forward.argtypes = [_P, _P, _I, _I, _I, _QP, _QP, _QP, _I, _I, _P, ctypes.c_size_t, _P, _P]
+    lib.ffn_moe_route.restype = _I
+    lib.ffn_moe_route.argtypes = [_P, _I, _I, _I, _P, _I, _I, _I, ctypes.c_float, _P, _P, _P]
+    lib.ffn_moe_plan_workspace_bytes.restype = ctypes.c_size_t
+    lib.ffn_moe_plan_workspace_bytes.argtypes = [_I, _I, _I]
+    lib.ffn_moe_plan.restype = _I
+    lib.ffn_moe_plan.argtypes = [_P, _I, _I, _I, _P, _P, _P, _P, ctypes.c_size_t, _P]
+    lib.ffn_moe_gemm.restype = _I
+    lib.ffn_moe_gemm.argtypes = [_P, _I, _I, _P, _I, _P, _I, _I, _I, _I, _EP, _I, _P, _P]
+    lib.ffn_moe_workspace_bytes.restype = ctypes.c_size_t
+    lib.ffn_moe_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
+    lib.ffn_moe_forward.restype = _I
+    lib.ffn_moe_forward.argtypes = [_P, _I, _I, _I, _I, _I, _I, _P, _P, _EP, _EP, _EP, _I, _P, ctypes.c_size_t, _P,
+                                    _P]
     _lib = lib
     return lib
 
@@ -195,7 +227,7 @@ def header_functions(path: str = HEADER_PATH) -> Sequence[str]:
     import re
     text = open(path).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(ffn_(?:nvfp4|fp8|w4a4|int8|diag)_[a-z_0-9]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(ffn_(?:nvfp4|fp8|w4a4|int8|moe|diag)_[a-z_0-9]+)\s*\(", text)))
 
 
 def version() -> int:
@@ -953,6 +985,219 @@ def int8_forward(xq, xs, gate: Int8DeviceWeight, up: Int8DeviceWeight, down: Int
                               ctypes.byref(d), int(act), dtype, workspace.data_ptr(),
                               workspace.numel() * workspace.element_size(), out.data_ptr(), _stream_handle(stream))
     _check(rc, "ffn_int8_forward")
+    return out
+
+
+# ------------------------------------------------------------ sparse FFN (mixture of experts)
+
+
+@dataclasses.dataclass
+class MoeDeviceWeight:
+    """NVFP4 weights of E experts on the GPU: codes uint8 [E, rows, cols/2],
+    scales uint8 [E, rows, cols/16], scale2 float32 [E]."""
+
+    codes: "object"
+    scales: "object"
+    scale2: "object"
+
+    @property
+    def experts(self) -> int:
+        return int(self.codes.shape[0])
+
+    @property
+    def rows(self) -> int:
+        return int(self.codes.shape[1])
+
+    @property
+    def cols(self) -> int:
+        return int(self.codes.shape[2]) * 2
+
+    def struct(self) -> MoeWeightStruct:
+        return MoeWeightStruct(self.codes.data_ptr(), self.scales.data_ptr(), self.scale2.data_ptr())
+
+    @classmethod
+    def stack(cls, weights: Sequence[DeviceWeight]) -> "MoeDeviceWeight":
+        """From one :class:`DeviceWeight` for each expert (copies them)."""
+        import torch
+        dev = weights[0].codes.device
+        return cls(torch.stack([w.codes for w in weights]), torch.stack([w.scales for w in weights]),
+                   torch.tensor([w.scale2 for w in weights], dtype=torch.float32, device=dev))
+
+
+def _check_moe_weight(w: MoeDeviceWeight, experts: int, rows: int, cols: int, name: str, device) -> None:
+    """NVFP4 weights of logical shape [experts, rows, cols] on the device of the call."""
+    import torch
+    c, s, s2 = w.codes, w.scales, w.scale2
+    if cols % 16:
+        raise ValueError(f"{name}: {cols} columns is not a multiple of 16")
+    if (c.dtype == torch.uint8 and c.shape == (experts, rows, cols // 2) and c.is_contiguous() and c.device == device
+            and s.dtype == torch.uint8 and s.shape == (experts, rows, cols // 16) and s.is_contiguous()
+            and s.device == device and s2.dtype == torch.float32 and s2.shape == (experts,) and s2.is_contiguous()
+            and s2.device == device):
+        return
+    _check_tensor(c, torch.uint8, (experts, rows, cols // 2), f"{name}.codes", device)
+    _check_tensor(s, torch.uint8, (experts, rows, cols // 16), f"{name}.scales", device)
+    _check_tensor(s2, torch.float32, (experts,), f"{name}.scale2", device)
+
+
+def _check_current(device) -> None:
+    """The library launches on the current device, which has to be the tensors'."""
+    import torch
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _moe_half(dtype, name: str) -> int:
+    """ffn_moe_dtype of a 16-bit torch type."""
+    code = _int8_dtype(dtype, name)
+    if code > 1:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {dtype}")
+    return code
+
+
+def moe_route(logits, top_k: int, score: int = SCORE_SOFTMAX, bias=None, normalize: bool = True, scale: float = 1.0,
+              ids=None, weights=None, stream=None):
+    """(ids int32 [T, top_k], weights fp32 [T, top_k]): the experts of the
+    largest keys of each row of ``logits`` [T, E], the largest first, ties to
+    the lower expert, and their weights ``scale * score`` (``normalize``: over
+    the sum of the chosen scores). The key is the logit, or with ``bias`` (fp32
+    [E]) score + bias. Experts with a logit or key of -infinity are not
+    chosen: an id of -1 with weight 0 stands where too few are left."""
+    import torch
+    T, E = logits.shape
+    dev = logits.device
+    dtype = _int8_dtype(logits.dtype, "logits")
+    _check_tensor(logits, logits.dtype, (T, E), "logits")
+    if bias is not None:
+        _check_tensor(bias, torch.float32, (E,), "bias", dev)
+    if ids is None:
+        ids = _empty((T, top_k), torch.int32, dev, stream)
+    else:
+        _check_tensor(ids, torch.int32, (T, top_k), "ids", dev)
+    if weights is None:
+        weights = _empty((T, top_k), torch.float32, dev, stream)
+    else:
+        _check_tensor(weights, torch.float32, (T, top_k), "weights", dev)
+    _check_current(dev)
+    rc = load().ffn_moe_route(logits.data_ptr(), T, E, dtype, None if bias is None else bias.data_ptr(), top_k,
+                              int(score), bool(normalize), scale, ids.data_ptr(), weights.data_ptr(),
+                              _stream_handle(stream))
+    _check(rc, "ffn_moe_route")
+    return ids, weights
+
+
+def moe_plan_workspace_bytes(T: int, top_k: int, experts: int) -> int:
+    return int(load().ffn_moe_plan_workspace_bytes(int(T), int(top_k), int(experts)))
+
+
+def moe_plan(ids, experts: int, rows=None, offsets=None, places=None, workspace=None, stream=None):
+    """(rows int32 [T * top_k], offsets int32 [experts + 1], places int32 [T,
+    top_k]): the slots t * top_k + j of ``ids`` int32 [T, top_k] in expert order
+    (-1 behind the last expert's), where each expert begins, and the place of
+    each slot (-1: its id is no expert)."""
+    import torch
+    T, top_k = ids.shape
+    dev = ids.device
+    _check_tensor(ids, torch.int32, (T, top_k), "ids")
+    if rows is None:
+        rows = _empty((T * top_k,), torch.int32, dev, stream)
+    else:
+        _check_tensor(rows, torch.int32, (T * top_k,), "rows", dev)
+    if offsets is None:
+        offsets = _empty((experts + 1,), torch.int32, dev, stream)
+    else:
+        _check_tensor(offsets, torch.int32, (experts + 1,), "offsets", dev)
+    if places is None:
+        places = _empty((T, top_k), torch.int32, dev, stream)
+    else:
+        _check_tensor(places, torch.int32, (T, top_k), "places", dev)
+    lib = load()
+    if workspace is None:
+        need = lib.ffn_moe_plan_workspace_bytes(T, top_k, experts)
+        if need:
+            workspace = _empty((need,), torch.uint8, dev, stream)
+    else:
+        _check_workspace(workspace, dev)
+    _check_current(dev)
+    rc = lib.ffn_moe_plan(ids.data_ptr(), T, top_k, experts, rows.data_ptr(), offsets.data_ptr(), places.data_ptr(),
+                          None if workspace is None else workspace.data_ptr(),
+                          0 if workspace is None else workspace.numel() * workspace.element_size(),
+                          _stream_handle(stream))
+    _check(rc, "ffn_moe_plan")
+    return rows, offsets, places
+
+
+def moe_gemm(x, offsets, w: MoeDeviceWeight, rows=None, top_k: int = 1, out_dtype=None, out=None, stream=None):
+    """out[i] = w.scale2[e] * W_e x[i] for offsets[e] <= i < offsets[e + 1]
+    (``offsets`` int32 [E + 1], ascending, on the device); with ``rows`` int32
+    [R], slots of ``top_k`` for each row of x, out[i] is of x[rows[i] // top_k].
+    ``out_dtype``: x's type (the default) or float32. Rows of ``out`` outside
+    all experts are left as they were."""
+    import torch
+    x_rows, K = x.shape
+    E, N = w.experts, w.rows
+    dev = x.device
+    dtype = _moe_half(x.dtype, "x")
+    _check_tensor(x, x.dtype, (x_rows, K), "x")
+    _check_tensor(offsets, torch.int32, (E + 1,), "offsets", dev)
+    _check_moe_weight(w, E, N, K, "w", dev)
+    R = x_rows
+    if rows is not None:
+        R = rows.numel()
+        _check_tensor(rows, torch.int32, (R,), "rows", dev)
+    if out_dtype is None:
+        out_dtype = x.dtype if out is None else out.dtype
+    if out_dtype != x.dtype and out_dtype != torch.float32:
+        raise ValueError(f"out must be {x.dtype} or float32, got {out_dtype}")
+    if out is None:
+        out = _empty((R, N), out_dtype, dev, stream)
+    else:
+        _check_tensor(out, out_dtype, (R, N), "out", dev)
+    _check_current(dev)
+    st = w.struct()
+    rc = load().ffn_moe_gemm(x.data_ptr(), x_rows, dtype, None if rows is None else rows.data_ptr(), top_k,
+                             offsets.data_ptr(), R, E, K, N, ctypes.byref(st), 2 if out_dtype == torch.float32 else dtype,
+                             out.data_ptr(), _stream_handle(stream))
+    _check(rc, "ffn_moe_gemm")
+    return out
+
+
+def moe_workspace_bytes(T: int, top_k: int, experts: int, K: int, N: int) -> int:
+    return int(load().ffn_moe_workspace_bytes(int(T), int(top_k), int(experts), int(K), int(N)))
+
+
+def moe_forward(x, ids, weights, gate: MoeDeviceWeight, up: MoeDeviceWeight, down: MoeDeviceWeight,
+                act: int = ACT_SILU, out=None, workspace=None, stream=None):
+    """out[t] = sum_j weights[t, j] * W_d,e (act(W_g,e x[t]) * (W_u,e x[t])),
+    e = ids[t, j], for x [T, K] (bfloat16 or float16), ids int32 and weights fp32
+    [T, top_k]; an id outside 0 .. E - 1 adds nothing."""
+    import torch
+    T, K = x.shape
+    top_k = ids.shape[1]
+    E, N = gate.experts, gate.rows
+    dev = x.device
+    dtype = _moe_half(x.dtype, "x")
+    _check_tensor(x, x.dtype, (T, K), "x")
+    _check_tensor(ids, torch.int32, (T, top_k), "ids", dev)
+    _check_tensor(weights, torch.float32, (T, top_k), "weights", dev)
+    _check_moe_weight(gate, E, N, K, "gate", dev)
+    _check_moe_weight(up, E, N, K, "up", dev)
+    _check_moe_weight(down, E, K, N, "down", dev)
+    if out is None:
+        out = _empty((T, K), x.dtype, dev, stream)
+    else:
+        _check_tensor(out, x.dtype, (T, K), "out", dev)
+    lib = load()
+    if workspace is None:
+        workspace = _empty((max(lib.ffn_moe_workspace_bytes(T, top_k, E, K, N), 1),), torch.uint8, dev, stream)
+    else:
+        _check_workspace(workspace, dev)
+    _check_current(dev)
+    g, u, d = gate.struct(), up.struct(), down.struct()
+    rc = lib.ffn_moe_forward(x.data_ptr(), T, K, N, E, top_k, dtype, ids.data_ptr(), weights.data_ptr(),
+                             ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), int(act), workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), out.data_ptr(), _stream_handle(stream))
+    _check(rc, "ffn_moe_forward")
     return out
 
 
