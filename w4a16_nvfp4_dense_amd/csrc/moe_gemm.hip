@@ -27,72 +27,14 @@
 
 #include "kernels.h"
 #include "moe.h"
-#include "nvfp4_device.h"
+#include "moe_device.h"
+#include "moe_stream.h"
 
 namespace ffn {
 namespace {
 
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-
 constexpr int kThreads = 256;
 constexpr int kStageCols = 128;
-
-// Four bytes at any even address.
-struct __attribute__((packed, aligned(2))) pair16_t {
-    uint32_t both;
-};
-
-// What pieces past the last column are loaded from.
-__device__ const u32x4_t kZeros = {0, 0, 0, 0};
-
-// The element type's operations.
-template <class T>
-struct Half;
-template <>
-struct Half<__bf16> {
-    typedef bf16x8_t vec8;
-    // Eight codes times a block scale: exact, so the upper halves of the fp32
-    // products are the bf16 values.
-    static __device__ __forceinline__ vec8 weights(uint32_t codes, float scale)
-    {
-        const f32x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0);
-        const f32x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1);
-        const f32x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2);
-        const f32x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
-        const u32x4_t w = {upper(p0, scale), upper(p1, scale), upper(p2, scale), upper(p3, scale)};
-        return __builtin_bit_cast(vec8, w);
-    }
-    static __device__ __forceinline__ f32x16_t mfma(const vec8 &a, const vec8 &b, const f32x16_t &c)
-    {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-    }
-
-private:
-    static __device__ __forceinline__ uint32_t upper(const f32x2_t &p, float scale)
-    {
-        return __builtin_amdgcn_perm(__float_as_uint(p[1] * scale), __float_as_uint(p[0] * scale), 0x07060302u);
-    }
-};
-template <>
-struct Half<_Float16> {
-    typedef f16x8_t vec8;
-    static __device__ __forceinline__ vec8 weights(uint32_t codes, float scale)
-    {
-        const _Float16 s = static_cast<_Float16>(scale);
-        const f16x2_t s2 = {s, s};
-        const f16x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 0) * s2;
-        const f16x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 1) * s2;
-        const f16x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 2) * s2;
-        const f16x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, 3) * s2;
-        return vec8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-    }
-    static __device__ __forceinline__ f32x16_t mfma(const vec8 &a, const vec8 &b, const f32x16_t &c)
-    {
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
-    }
-};
 
 // The tile of a workgroup.
 struct Tile {
@@ -100,13 +42,6 @@ struct Tile {
     int begin, end;  // its rows of the product
     int nt;          // which channels
 };
-
-// An expert's rows, whatever the offsets hold.
-__device__ __forceinline__ void rows_of(const MoeGemmArgs &a, int e, int &begin, int &end)
-{
-    begin = min(max(a.offsets[e], 0), a.R);
-    end = min(max(a.offsets[e + 1], begin), a.R);
-}
 
 // Finds tile number `at` (of this workgroup, see above) among tiles of BM rows
 // and `nts` groups of channels. Every thread calls it; it has barriers.
@@ -354,23 +289,12 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
             const int i = tile.begin + 32 * mt + 8 * (v >> 2) + 4 * h + (v & 3);
             if (i >= tile.end)
                 continue;
-            const float y0 = acc[0][mt][v] * s0, y1 = acc[1][mt][v] * s1;
+            const float y0 = acc[0][mt][v], y1 = acc[1][mt][v];
             const size_t o = static_cast<size_t>(i) * N + n0;
-            if constexpr (TWO) {
-                constexpr int A = OUT == MOE_H_SILU ? ACT_SILU : ACT_GELU_TANH;
-                if (n0 < N)
-                    static_cast<T *>(a.out)[o] = static_cast<T>(gate_act<A>(y0) * y1);
-            } else if constexpr (OUT == MOE_F32) {
-                if (n0 < N)
-                    static_cast<float *>(a.out)[o] = y0;
-                if (n0 + 32 < N)
-                    static_cast<float *>(a.out)[o + 32] = y1;
-            } else {
-                if (n0 < N)
-                    static_cast<T *>(a.out)[o] = static_cast<T>(y0);
-                if (n0 + 32 < N)
-                    static_cast<T *>(a.out)[o + 32] = static_cast<T>(y1);
-            }
+            if (n0 < N)
+                moe_store<T, OUT>(a.out, o, moe_value<OUT>(y0, y1, s0, s1));
+            if (!TWO && n0 + 32 < N)
+                moe_store<T, OUT>(a.out, o + 32, moe_value<OUT>(y1, 0.0f, s0, s1));
         }
 }
 
@@ -394,6 +318,9 @@ hipError_t launch_tiles(const MoeGemmArgs &a, hipStream_t stream)
 template <class T, int OUT>
 hipError_t launch_out(const MoeGemmArgs &a, hipStream_t stream)
 {
+    const hipError_t e = launch_moe_stream<T, OUT>(a, stream);
+    if (e != hipErrorNotSupported)
+        return e;
     const int mean = a.R / a.E;  // rows of an expert
     if (mean > 64)
         return launch_tiles<T, 4, OUT>(a, stream);
