@@ -78,6 +78,26 @@ struct Half<_Float16> {
     }
 };
 
+// A load from global memory of an address that was chosen between two. (Without
+// the address space the compiler takes it for any memory's, and waits for all
+// loads in flight where one such is among them.)
+template <class V>
+__device__ __forceinline__ V load_global(uintptr_t at)
+{
+    return *(const __attribute__((address_space(1))) V *)at;
+}
+
+// A buffer whose base and size are the same in all lanes, which the compiler
+// does not always see.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_buffer(const void *base, int bytes)
+{
+    const uint64_t at = reinterpret_cast<uintptr_t>(base);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
+    return raw_buffer(reinterpret_cast<const void *>(static_cast<uint64_t>(hi) << 32 | lo),
+                      __builtin_amdgcn_readfirstlane(bytes));
+}
+
 // An expert's rows, whatever the offsets hold.
 __device__ __forceinline__ void rows_of(const MoeGemmArgs &a, int e, int &begin, int &end)
 {

@@ -4,8 +4,8 @@
 //
 // A tile is 16 rows of one expert (the matrix cores' smallest; rows that are not
 // there cost nothing but idle lanes). Eight waves of a workgroup share its
-// reduction: wave w takes the 128-column chunks w, w + 8, ... of every weight
-// row, and keeps the tile's activations of those columns in registers. A pass
+// reduction: each takes some 128-column chunks of every weight row, and keeps
+// the tile's activations of those columns in registers. A pass
 // is 32 weight rows (16 channels of two weights): each wave multiplies its
 // chunks of them, the eight partial sums meet in LDS, and one thread finishes
 // each result. The weights of the next pass are loaded before those of the
@@ -28,6 +28,7 @@ constexpr int kStreamThreads = kStreamWaves * 64;
 constexpr int kStreamChunk = 128;  // columns of a wave's chunk
 constexpr int kStreamMostChunks = 6;
 constexpr int kMoeMostExperts = 1024;
+constexpr int kPast = 1 << 30;  // a byte offset past any buffer of rows
 
 // Tiles of 16 rows of experts before this thread's (it has experts 2 tid and
 // 2 tid + 1), and of all. Every thread of the workgroup calls it.
@@ -53,12 +54,15 @@ __device__ __forceinline__ int stream_tiles_before(int mine, int *wave_sum, int 
     return sum;
 }
 
-// CH: chunks of a wave.
-template <class T, int CH, int OUT>
+// WK: waves that share a reduction (the workgroup's 8 / WK groups of them have
+// 32 weight rows of a pass each). CH: chunks of a wave.
+template <class T, int WK, int CH, int OUT>
 __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_kernel(const MoeGemmArgs a)
 {
     constexpr bool TWO = moe_two_weights(OUT);
-    constexpr int BN = TWO ? 16 : 32;  // channels of a pass
+    constexpr int GROUPS = kStreamWaves / WK;
+    constexpr int GN = TWO ? 16 : 32;   // channels of a group
+    constexpr int BN = GN * GROUPS;     // and of a pass
     typedef typename Half<T>::vec8 vec8;
 
     __shared__ int begins[kMoeMostExperts + 1];  // where the experts' rows begin
@@ -70,8 +74,11 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q = lane >> 4, r = lane & 15;
+    const int wk = wave % WK, group = wave / WK;
     const int K = a.K, N = a.N;
     const int passes = (N + BN - 1) / BN;  // of a tile
+
+    const auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
 
     // This workgroup's run of passes.
     int mine = 0;
@@ -88,9 +95,11 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     }
     int total;
     const int before = stream_tiles_before(mine, wave_sum, total);
-    const long all = static_cast<long>(total) * passes;
-    const long from = all * blockIdx.x / gridDim.x, to = all * (blockIdx.x + 1) / gridDim.x;
-    if (from == to)
+    const unsigned all = static_cast<unsigned>(total) * passes;  // (below 2^31: see the launcher)
+    const unsigned share = all / gridDim.x, over = all % gridDim.x, b = blockIdx.x;
+    const unsigned from = b * share + min(b, over);
+    const int count = scalar(share + (b < over ? 1 : 0));
+    if (count == 0)
         return;
     const int first = static_cast<int>(from / passes);  // the run's first tile
     if (first >= before && first < before + mine) {
@@ -104,40 +113,63 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
         start[1] = t;
     }
     __syncthreads();
-    const auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     int e = scalar(start[0]);
-    int row0 = scalar(begins[e]) + scalar(start[1]) * kStreamRows, row_end = scalar(ends[e]);
-    int pass = scalar(static_cast<int>(from - static_cast<long>(first) * passes));
-    int left = scalar(static_cast<int>(to - from));
+    int row_end = scalar(ends[e]), row0 = scalar(begins[e] + start[1] * kStreamRows);
+    int pass = scalar(static_cast<int>(from) - first * passes);  // (divisions run on the vector unit)
+    int left = count;
 
-    // Chunk i of this lane: columns 128 (w + 8 i) + 32 q .. + 31. The last of a
-    // wave's chunks may lie past the end: then its weights and activations are
-    // zeros (and the addresses those of column 0).
-    const int col0 = wave * kStreamChunk + 32 * q;
-    const bool there = col0 + (CH - 1) * kStreamWaves * kStreamChunk < K;
-    const auto col_of = [&](int i) { return i == CH - 1 && !there ? 0 : col0 + i * kStreamWaves * kStreamChunk; };
+    // Chunks go in pairs, so that a lane has 64 consecutive columns of a row with
+    // their four scale bytes: chunks 2 j and 2 j + 1 are its columns 256 (w + WK j)
+    // + 64 q .. + 31 and .. + 63; the last chunk of an odd number is columns 128
+    // (WK (CH - 1) + w) + 32 q .. + 31. Only those of the last pair, or the odd
+    // chunk, may lie past the end.
+    constexpr int PAIRS = CH / 2;
+    constexpr int LAST = CH % 2 ? CH - 1 : CH - 2;  // first chunk that may be past the end
+    const int pair0 = wk * 256 + 64 * q;
+    const int last0 = CH % 2 ? (CH - 1) * WK * 128 + wk * 128 + 32 * q : pair0 + (PAIRS - 1) * WK * 256;
+    const auto col_of = [&](int i) {
+        return i < LAST ? pair0 + (i / 2) * WK * 256 + i % 2 * 32 : last0 + (i - LAST) * 32;
+    };
 
     // The weight rows of a pass in registers: 32 columns of one row for each
-    // fragment and chunk.
+    // fragment and chunk, two chunks' scales in a register. They are loaded by
+    // buffer, whose bounds check gives zeros for rows past the last channel (and
+    // for the pass behind the run's last, of no rows: the same number of loads
+    // on every path, so that the compiler's waits for the pass at hand are not
+    // waits for the next one); columns past the end have an offset past any
+    // buffer. Of a pair whose second chunk is past the end, the scales are
+    // loaded two bytes earlier, so as to end with the row, and shifted.
     struct Rows {
         u32x4_t codes[2][CH];
-        uint32_t scales[2][CH];
+        uint32_t scales[2][(CH + 1) / 2];
     };
-    const size_t row_codes = static_cast<size_t>(K) / 2, row_scales = static_cast<size_t>(K) / 16;
-    const auto load = [&](Rows &w, int expert, int p) {
+    const int row_codes = K / 2, row_scales = K / 16;
+    const bool half = CH % 2 == 0 && last0 < K && last0 + 32 >= K;
+    int code_at[CH], scale_at[(CH + 1) / 2];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        code_at[i] = col_of(i) < K ? r * row_codes + col_of(i) / 2 : kPast;
+        if (i % 2 == 0)
+            scale_at[i / 2] = col_of(i) < K ? r * row_scales + col_of(i) / 16 - (i == LAST && half ? 2 : 0) : kPast;
+    }
+    const auto load = [&](Rows &w, int expert, int p, bool real) {
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            const uint8_t *codes = TWO && f == 1 ? a.w1.codes : a.w0.codes;
-            const uint8_t *scales = TWO && f == 1 ? a.w1.scales : a.w0.scales;
-            const int n = min(p * BN + (TWO ? 0 : 16 * f) + r, N - 1);
-            const size_t row = static_cast<size_t>(expert) * N + n;
+            const int n = scalar(p) * BN + group * GN + (TWO ? 0 : 16 * f);
+            const size_t row = static_cast<size_t>(scalar(expert)) * N + n;
+            const int rows = real ? min(max(N - n, 0), 16) : 0;
+            const auto codes = uniform_buffer((TWO && f == 1 ? a.w1.codes : a.w0.codes) + row * row_codes, rows * row_codes);
+            const auto scales =
+                uniform_buffer((TWO && f == 1 ? a.w1.scales : a.w0.scales) + row * row_scales, rows * row_scales);
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int col = col_of(i);
-                w.codes[f][i] = *reinterpret_cast<const u32x4_t *>(codes + row * row_codes + col / 2);
-                w.scales[f][i] = *reinterpret_cast<const uint16_t *>(scales + row * row_scales + col / 16);
-            }
+            for (int i = 0; i < CH; ++i)
+                w.codes[f][i] = __builtin_amdgcn_raw_buffer_load_b128(codes, code_at[i], 0, 0);
+#pragma unroll
+            for (int j = 0; j < (CH + 1) / 2; ++j)
+                w.scales[f][j] = 2 * j + 1 == CH ? __builtin_amdgcn_raw_buffer_load_b16(scales, scale_at[j], 0, 0)
+                                                 : __builtin_amdgcn_raw_buffer_load_b32(scales, scale_at[j], 0, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);  // (nothing that waits for earlier loads goes before these)
     };
     vec8 x[CH][4];
     float s0 = 0.0f, s1 = 0.0f;
@@ -149,11 +181,9 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
 #pragma unroll
         for (int i = 0; i < CH; ++i)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                x[i][t] = *reinterpret_cast<const vec8 *>(xr + col_of(i) + 8 * t);
-                if (i == CH - 1 && !there)
-                    x[i][t] = vec8{};
-            }
+            for (int t = 0; t < 4; ++t)
+                x[i][t] = load_global<vec8>(col_of(i) < K ? reinterpret_cast<uintptr_t>(xr + col_of(i) + 8 * t)
+                                                          : reinterpret_cast<uintptr_t>(&kZeros));
         s0 = a.w0.scale2[e];
         s1 = TWO ? a.w1.scale2[e] : s0;
     };
@@ -182,9 +212,9 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
         for (int i = 0; i < CH; ++i)
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-                const bool zero = i == CH - 1 && !there;
-                const float sc0 = zero ? 0.0f : e4m3_to_f32<0>(w.scales[f][i]);
-                const float sc1 = zero ? 0.0f : e4m3_to_f32<1>(w.scales[f][i]);
+                const uint32_t both = i >= LAST && half ? w.scales[f][i / 2] >> 16 : w.scales[f][i / 2];
+                const float sc0 = i % 2 ? e4m3_to_f32<2>(both) : e4m3_to_f32<0>(both);
+                const float sc1 = i % 2 ? e4m3_to_f32<3>(both) : e4m3_to_f32<1>(both);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     acc[f] = Half<T>::mfma(x[i][t], Half<T>::weights(w.codes[f][i][t], t < 2 ? sc0 : sc1), acc[f]);
@@ -194,19 +224,23 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
             part[parity][f][wave][lane] = acc[f];
     };
     // One thread for each result: value c of lane l is row 4 (l / 16) + c of
-    // channel l % 16. Threads 256 .. 511 have the second fragment's.
+    // channel l % 16 of a fragment.
     const auto finish = [&]() {
         lds_barrier();
-        const int j = threadIdx.x & 255, f = threadIdx.x >> 8;
-        const int l = j & 63, c = j >> 6;
-        const int row = row0 + 4 * (l >> 4) + c, n = pass * BN + (TWO ? 0 : 16 * f) + (l & 15);
-        float sum0 = 0.0f, sum1 = 0.0f;
-        if (!(TWO && f == 1)) {
 #pragma unroll
-            for (int w = 0; w < kStreamWaves; ++w) {
-                sum0 += reinterpret_cast<const float *>(&part[parity][f][w][l])[c];
+        for (int k = 0; k < GROUPS * (TWO ? 1 : 2); k += 2) {
+            const int j = threadIdx.x & 255, i = k + (threadIdx.x >> 8);  // i: which 256 results
+            if (TWO && GROUPS == 1 && i == 1)
+                break;
+            const int f = TWO ? 0 : i & 1, g = TWO ? i : i >> 1;
+            const int l = j & 63, c = j >> 6;
+            const int row = row0 + 4 * (l >> 4) + c, n = pass * BN + g * GN + 16 * f + (l & 15);
+            float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WK; ++w) {
+                sum0 += reinterpret_cast<const float *>(&part[parity][f][g * WK + w][l])[c];
                 if (TWO)
-                    sum1 += reinterpret_cast<const float *>(&part[parity][1][w][l])[c];
+                    sum1 += reinterpret_cast<const float *>(&part[parity][1][g * WK + w][l])[c];
             }
             if (row < row_end && n < N)
                 moe_store<T, OUT>(a.out, static_cast<size_t>(row) * N + n, moe_value<OUT>(sum0, sum1, s0, s1));
@@ -215,12 +249,11 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     };
 
     Rows even, odd;
-    load(even, e, pass);
+    load(even, e, pass, true);
     load_tile();
     const auto step = [&](Rows &now, Rows &next) {
         find_next();
-        if (left > 1)
-            load(next, next_e, next_pass);
+        load(next, next_e, next_pass, left > 1);
         multiply(now);
         finish();
         const bool tile = next_pass == 0;
@@ -242,13 +275,19 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     }
 }
 
-template <class T, int CH, int OUT>
+// The most passes that a product can have.
+template <int OUT>
+long stream_passes(const MoeGemmArgs &a, int WK)
+{
+    const int BN = (moe_two_weights(OUT) ? 16 : 32) * kStreamWaves / WK;
+    return (a.R / kStreamRows + (a.R < a.E ? a.R : a.E)) * static_cast<long>((a.N + BN - 1) / BN);
+}
+
+template <class T, int WK, int CH, int OUT>
 hipError_t launch_stream_chunks(const MoeGemmArgs &a, hipStream_t stream)
 {
-    constexpr int BN = moe_two_weights(OUT) ? 16 : 32;
-    const long most = (a.R / kStreamRows + (a.R < a.E ? a.R : a.E)) * static_cast<long>((a.N + BN - 1) / BN);
-    const long room = device_cu_count() * (CH <= 2 ? 2 : 1);
-    hipLaunchKernelGGL((moe_stream_kernel<T, CH, OUT>), dim3(most < room ? most : room), dim3(kStreamThreads), 0,
+    const long most = stream_passes<OUT>(a, WK), room = device_cu_count() * (CH <= 2 ? 2 : 1);
+    hipLaunchKernelGGL((moe_stream_kernel<T, WK, CH, OUT>), dim3(most < room ? most : room), dim3(kStreamThreads), 0,
                        stream, a);
     return hipGetLastError();
 }
@@ -258,21 +297,23 @@ hipError_t launch_stream_chunks(const MoeGemmArgs &a, hipStream_t stream)
 template <class T, int OUT>
 hipError_t launch_moe_stream(const MoeGemmArgs &a, hipStream_t stream)
 {
-    if (a.R > 16 * a.E)
+    if (a.R > 16 * a.E || a.K < 64)
         return hipErrorNotSupported;
     switch ((a.K + kStreamWaves * kStreamChunk - 1) / (kStreamWaves * kStreamChunk)) {
     case 1:
-        return launch_stream_chunks<T, 1, OUT>(a, stream);
+        if (a.K > 512 && stream_passes<OUT>(a, 4) >= 4 * device_cu_count())
+            return launch_stream_chunks<T, 4, 2, OUT>(a, stream);
+        return launch_stream_chunks<T, 8, 1, OUT>(a, stream);
     case 2:
-        return launch_stream_chunks<T, 2, OUT>(a, stream);
+        return launch_stream_chunks<T, 8, 2, OUT>(a, stream);
     case 3:
-        return launch_stream_chunks<T, 3, OUT>(a, stream);
+        return launch_stream_chunks<T, 8, 3, OUT>(a, stream);
     case 4:
-        return launch_stream_chunks<T, 4, OUT>(a, stream);
+        return launch_stream_chunks<T, 8, 4, OUT>(a, stream);
     case 5:
-        return launch_stream_chunks<T, 5, OUT>(a, stream);
+        return launch_stream_chunks<T, 8, 5, OUT>(a, stream);
     case 6:
-        return launch_stream_chunks<T, 6, OUT>(a, stream);
+        return launch_stream_chunks<T, 8, 6, OUT>(a, stream);
     default:
         return hipErrorNotSupported;
     }
