@@ -164,7 +164,7 @@ int ffn_moe_gemm(const void *x, int x_rows, int dtype, const int32_t *rows, int 
         return FFN_NVFP4_ERR_NULL;
     if (!aligned(x, 16) || !aligned(rows, 4) || !aligned(offsets, 4) || !aligned(out, 16))
         return FFN_NVFP4_ERR_ALIGN;
-    const ffn::MoeGemmArgs a{x, rows, offsets, weight(w), {}, out, x_rows, top_k, R, E, K, N};
+    const ffn::MoeGemmArgs a{x, rows, offsets, nullptr, weight(w), {}, out, x_rows, top_k, R, E, K, N};
     return launch_status(
         ffn::launch_moe_gemm(a, dtype, out_dtype == FFN_MOE_F32 ? ffn::MOE_F32 : ffn::MOE_SAME, stream));
 }
@@ -201,18 +201,22 @@ int ffn_moe_forward(const void *x, int T, int K, int N, int E, int top_k, int dt
     int32_t *offsets = reinterpret_cast<int32_t *>(ws + w.offsets);
     int32_t *places = reinterpret_cast<int32_t *>(ws + w.places);
     const int R = T * top_k;
-    hipError_t e = ffn::launch_moe_plan(ids, R, E, rows, offsets, places, ws + w.plan, stream);
+    const ffn::MoeOut gated = act == FFN_NVFP4_ACT_SILU ? ffn::MOE_H_SILU : ffn::MOE_H_GELU;
+    const bool by_slots = ffn::moe_by_slots(R, E, K, N);
+    hipError_t e = by_slots ? hipSuccess
+                            : ffn::launch_moe_plan(ids, R, E, rows, offsets, places, ws + w.plan, stream);
     if (e != hipSuccess)
         return FFN_NVFP4_ERR_LAUNCH;
-    const ffn::MoeGemmArgs dual{x, rows, offsets, weight(gate), weight(up), ws + w.h, T, top_k, R, E, K, N};
-    e = ffn::launch_moe_gemm(dual, dtype, act == FFN_NVFP4_ACT_SILU ? ffn::MOE_H_SILU : ffn::MOE_H_GELU, stream);
-    if (e != hipSuccess)
+    // h and the experts' outputs are in expert order, or without a plan in that
+    // of the slots.
+    const int32_t *slots = by_slots ? ids : nullptr;
+    const ffn::MoeGemmArgs first{x, rows, offsets, slots, weight(gate), weight(up), ws + w.h, T, top_k, R, E, K, N};
+    const ffn::MoeGemmArgs last{ws + w.h, nullptr, offsets, slots, weight(down), {}, ws + w.y, R, 1, R, E, N, K};
+    if ((e = ffn::launch_moe_gemm(first, dtype, gated, stream)) != hipSuccess ||
+        (e = ffn::launch_moe_gemm(last, dtype, ffn::MOE_SAME, stream)) != hipSuccess)
         return FFN_NVFP4_ERR_LAUNCH;
-    const ffn::MoeGemmArgs last{ws + w.h, nullptr, offsets, weight(down), {}, ws + w.y, R, 1, R, E, N, K};
-    e = ffn::launch_moe_gemm(last, dtype, ffn::MOE_SAME, stream);
-    if (e != hipSuccess)
-        return FFN_NVFP4_ERR_LAUNCH;
-    return launch_status(ffn::launch_moe_combine(ws + w.y, places, weights, T, top_k, R, K, dtype, out, stream));
+    return launch_status(
+        ffn::launch_moe_combine(ws + w.y, places, slots, weights, T, top_k, R, E, K, dtype, out, stream));
 }
 
 }  // extern "C"

@@ -30,9 +30,10 @@ hipError_t launch_moe_plan(const int32_t *ids, int R, int E, int32_t *rows, int3
 
 // out[t] = sum_j weights[t, j] * y[places[t, j]] (moe_combine.hip), y and out
 // of `dtype` with K columns, K a multiple of 8; places outside 0 .. R - 1 are
-// skipped.
-hipError_t launch_moe_combine(const void *y, const int32_t *places, const float *weights, int T, int top_k, int R,
-                              int K, int dtype, void *out, hipStream_t stream);
+// skipped. With `ids` in place of places, y has a row for each slot; slots with
+// ids outside 0 .. E - 1 are skipped.
+hipError_t launch_moe_combine(const void *y, const int32_t *places, const int32_t *ids, const float *weights, int T,
+                              int top_k, int R, int E, int K, int dtype, void *out, hipStream_t stream);
 
 struct MoeWeightArg {
     const uint8_t *codes;   // [E, rows, cols/2]
@@ -58,10 +59,13 @@ struct MoeGemmArgs {
     const void *x;           // [x_rows, K]
     const int32_t *rows;     // [R] or null: row i of the product is x[rows[i] / top_k]
     const int32_t *offsets;  // [E + 1]
+    const int32_t *ids;      // or, without a plan, the experts of the R slots: row s is of x[s / top_k]
     MoeWeightArg w0, w1;     // [E, N, K]; w1 for two weights
     void *out;               // [R, N]
     int x_rows, top_k, R, E, K, N;
 };
+// Whether products of R slots over [N, K] and [K, N] may go without a plan.
+bool moe_by_slots(int R, int E, int K, int N);
 hipError_t launch_moe_gemm(const MoeGemmArgs &a, int dtype, MoeOut out, hipStream_t stream);
 
 }  // namespace ffn

@@ -1,5 +1,5 @@
 // moe_combine.hip -- the weighted sum of a token's experts' outputs:
-// out[t] = sum_j weights[t, j] y[places[t, j]], in fp32 with j ascending.
+// out[t] = sum_j weights[t, j] y[place of (t, j)], in fp32 with j ascending.
 //
 // It moves top_k rows in and one out for each token and computes almost
 // nothing. A thread has eight columns (16 bytes of every row) and asks for
@@ -17,15 +17,18 @@ constexpr int kAtOnce = 8;
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void moe_combine_kernel(const T *y, const int32_t *places,
-                                                               const float *weights, int top_k, int R, int K, T *out)
+                                                               const int32_t *ids, const float *weights, int top_k,
+                                                               int R, int E, int K, T *out)
 {
     typedef T vec8 __attribute__((ext_vector_type(8)));
     const int t = blockIdx.x;
     const int c = (blockIdx.y * kThreads + threadIdx.x) * 8;
     if (c >= K)
         return;
-    const int32_t *place = places + static_cast<size_t>(t) * top_k;
-    const float *weight = weights + static_cast<size_t>(t) * top_k;
+    const int slot = t * top_k;
+    const int32_t *place = (ids ? ids : places) + slot;
+    const int most = ids ? E : R;
+    const float *weight = weights + slot;
     float sum[8] = {};
     for (int j0 = 0; j0 < top_k; j0 += kAtOnce) {
         vec8 v[kAtOnce];
@@ -34,10 +37,10 @@ __global__ __launch_bounds__(kThreads) void moe_combine_kernel(const T *y, const
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const int at = j0 + j < top_k ? place[j0 + j] : -1;
-            there[j] = at >= 0 && at < R;
+            there[j] = at >= 0 && at < most;
             if (there[j]) {
                 w[j] = weight[j0 + j];
-                v[j] = *reinterpret_cast<const vec8 *>(y + static_cast<size_t>(at) * K + c);
+                v[j] = *reinterpret_cast<const vec8 *>(y + static_cast<size_t>(ids ? slot + j0 + j : at) * K + c);
             }
         }
 #pragma unroll
@@ -56,16 +59,17 @@ __global__ __launch_bounds__(kThreads) void moe_combine_kernel(const T *y, const
 
 }  // namespace
 
-hipError_t launch_moe_combine(const void *y, const int32_t *places, const float *weights, int T, int top_k, int R,
-                              int K, int dtype, void *out, hipStream_t stream)
+hipError_t launch_moe_combine(const void *y, const int32_t *places, const int32_t *ids, const float *weights, int T,
+                              int top_k, int R, int E, int K, int dtype, void *out, hipStream_t stream)
 {
     const dim3 grid(T, (K / 8 + kThreads - 1) / kThreads);
     if (dtype == kMoeBf16)
         hipLaunchKernelGGL((moe_combine_kernel<__bf16>), grid, dim3(kThreads), 0, stream,
-                           static_cast<const __bf16 *>(y), places, weights, top_k, R, K, static_cast<__bf16 *>(out));
+                           static_cast<const __bf16 *>(y), places, ids, weights, top_k, R, E, K,
+                           static_cast<__bf16 *>(out));
     else
         hipLaunchKernelGGL((moe_combine_kernel<_Float16>), grid, dim3(kThreads), 0, stream,
-                           static_cast<const _Float16 *>(y), places, weights, top_k, R, K,
+                           static_cast<const _Float16 *>(y), places, ids, weights, top_k, R, E, K,
                            static_cast<_Float16 *>(out));
     return hipGetLastError();
 }

@@ -318,9 +318,8 @@ hipError_t launch_tiles(const MoeGemmArgs &a, hipStream_t stream)
 template <class T, int OUT>
 hipError_t launch_out(const MoeGemmArgs &a, hipStream_t stream)
 {
-    const hipError_t e = launch_moe_stream<T, OUT>(a, stream);
-    if (e != hipErrorNotSupported)
-        return e;
+    if (a.R <= kStreamRows * a.E && stream_fits(a.K))
+        return launch_moe_stream<T, false, OUT>(a, stream);
     const int mean = a.R / a.E;  // rows of an expert
     if (mean > 64)
         return launch_tiles<T, 4, OUT>(a, stream);
@@ -329,22 +328,36 @@ hipError_t launch_out(const MoeGemmArgs &a, hipStream_t stream)
     return launch_tiles<T, 1, OUT>(a, stream);
 }
 
+template <class T, int OUT>
+hipError_t launch_either(const MoeGemmArgs &a, hipStream_t stream)
+{
+    if constexpr (OUT != MOE_F32)
+        if (a.ids)
+            return launch_moe_stream<T, true, OUT>(a, stream);
+    return launch_out<T, OUT>(a, stream);
+}
+
 template <class T>
 hipError_t launch_type(const MoeGemmArgs &a, MoeOut out, hipStream_t stream)
 {
     switch (out) {
     case MOE_SAME:
-        return launch_out<T, MOE_SAME>(a, stream);
+        return launch_either<T, MOE_SAME>(a, stream);
     case MOE_F32:
-        return launch_out<T, MOE_F32>(a, stream);
+        return launch_either<T, MOE_F32>(a, stream);
     case MOE_H_SILU:
-        return launch_out<T, MOE_H_SILU>(a, stream);
+        return launch_either<T, MOE_H_SILU>(a, stream);
     default:
-        return launch_out<T, MOE_H_GELU>(a, stream);
+        return launch_either<T, MOE_H_GELU>(a, stream);
     }
 }
 
 }  // namespace
+
+bool moe_by_slots(int R, int E, int K, int N)
+{
+    return R <= kStreamSlots && R <= kStreamRows * E && stream_fits(K) && stream_fits(N);
+}
 
 hipError_t launch_moe_gemm(const MoeGemmArgs &a, int dtype, MoeOut out, hipStream_t stream)
 {

@@ -27,6 +27,7 @@ constexpr int kStreamWaves = 8;
 constexpr int kStreamThreads = kStreamWaves * 64;
 constexpr int kStreamChunk = 128;  // columns of a wave's chunk
 constexpr int kStreamMostChunks = 6;
+constexpr int kStreamSlots = kStreamThreads;  // a thread for each
 constexpr int kMoeMostExperts = 1024;
 constexpr int kPast = 1 << 30;  // a byte offset past any buffer of rows
 
@@ -54,9 +55,13 @@ __device__ __forceinline__ int stream_tiles_before(int mine, int *wave_sum, int 
     return sum;
 }
 
+// SLOTS: there is no plan; a.ids has the experts of the R slots (at most
+// kStreamSlots), row s of the product is of x[s / top_k] and is written to
+// out[s]. Every workgroup counts the experts' slots for itself, and finds the
+// slots of a tile by looking through the ids, kept in LDS.
 // WK: waves that share a reduction (the workgroup's 8 / WK groups of them have
 // 32 weight rows of a pass each). CH: chunks of a wave.
-template <class T, int WK, int CH, int OUT>
+template <class T, bool SLOTS, int WK, int CH, int OUT>
 __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_kernel(const MoeGemmArgs a)
 {
     constexpr bool TWO = moe_two_weights(OUT);
@@ -67,6 +72,8 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
 
     __shared__ int begins[kMoeMostExperts + 1];  // where the experts' rows begin
     __shared__ int ends[kMoeMostExperts];
+    __shared__ int slot_ids[SLOTS ? kStreamSlots : 1];
+    __shared__ int tile_slots[SLOTS ? kStreamWaves : 1][kStreamRows];  // the tile's, for each wave
     __shared__ int wave_sum[kStreamWaves];
     __shared__ int start[2];  // expert and tile of it that the run begins with
     __shared__ f32x4_t part[2][2][kStreamWaves][64];  // partial sums: pass parity, fragment, wave, lane
@@ -82,14 +89,29 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
 
     // This workgroup's run of passes.
     int mine = 0;
+    if constexpr (SLOTS) {
+        // (begins is all zero, ends the number of slots)
+        for (int e = threadIdx.x; e < a.E; e += kStreamThreads)
+            begins[e] = ends[e] = 0;
+        const int id = static_cast<int>(threadIdx.x) < a.R ? a.ids[threadIdx.x] : -1;
+        slot_ids[threadIdx.x] = id;
+        __syncthreads();
+        if (id >= 0 && id < a.E)
+            atomicAdd(&ends[id], 1);
+        __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int e = 2 * threadIdx.x + i;
         if (e < a.E) {
-            int b, n;
-            rows_of(a, e, b, n);
-            begins[e] = b;
-            ends[e] = n;
+            int b = 0, n;
+            if constexpr (SLOTS) {
+                n = ends[e];
+            } else {
+                rows_of(a, e, b, n);
+                begins[e] = b;
+                ends[e] = n;
+            }
             mine += (n - b + kStreamRows - 1) / kStreamRows;
         }
     }
@@ -175,8 +197,21 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     float s0 = 0.0f, s1 = 0.0f;
     const auto load_tile = [&]() {
         int row = min(row0 + r, row_end - 1);
-        if (a.rows)
+        if constexpr (SLOTS) {
+            int rank = -row0;  // of the expert's slots, from the tile's first
+            for (int s0 = 0; s0 < a.R; s0 += 64) {
+                const bool ours = slot_ids[s0 + lane] == e;
+                const unsigned long long lanes = __ballot(ours);
+                const int at = rank + __popcll(lanes & ((1ull << lane) - 1));
+                if (ours && at >= 0 && at < kStreamRows)
+                    tile_slots[wave][at] = s0 + lane;
+                rank += __popcll(lanes);
+            }
+            __builtin_amdgcn_wave_barrier();
+            row = tile_slots[wave][row - row0] / a.top_k;
+        } else if (a.rows) {
             row = min(max(a.rows[row], 0) / a.top_k, a.x_rows - 1);
+        }
         const T *xr = static_cast<const T *>(a.x) + static_cast<size_t>(row) * K;
 #pragma unroll
         for (int i = 0; i < CH; ++i)
@@ -209,9 +244,9 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     const auto multiply = [&](const Rows &w) {
         f32x4_t acc[2] = {};
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
+        for (int f = 0; f < 2; ++f)  // (in the order of their loads)
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
+            for (int i = 0; i < CH; ++i) {
                 const uint32_t both = i >= LAST && half ? w.scales[f][i / 2] >> 16 : w.scales[f][i / 2];
                 const float sc0 = i % 2 ? e4m3_to_f32<2>(both) : e4m3_to_f32<0>(both);
                 const float sc1 = i % 2 ? e4m3_to_f32<3>(both) : e4m3_to_f32<1>(both);
@@ -235,6 +270,7 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
             const int f = TWO ? 0 : i & 1, g = TWO ? i : i >> 1;
             const int l = j & 63, c = j >> 6;
             const int row = row0 + 4 * (l >> 4) + c, n = pass * BN + g * GN + 16 * f + (l & 15);
+            const int to = SLOTS ? tile_slots[wave][row - row0] : row;
             float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
             for (int w = 0; w < WK; ++w) {
@@ -243,7 +279,7 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
                     sum1 += reinterpret_cast<const float *>(&part[parity][1][g * WK + w][l])[c];
             }
             if (row < row_end && n < N)
-                moe_store<T, OUT>(a.out, static_cast<size_t>(row) * N + n, moe_value<OUT>(sum0, sum1, s0, s1));
+                moe_store<T, OUT>(a.out, static_cast<size_t>(to) * N + n, moe_value<OUT>(sum0, sum1, s0, s1));
         }
         parity ^= 1;
     };
@@ -283,39 +319,39 @@ long stream_passes(const MoeGemmArgs &a, int WK)
     return (a.R / kStreamRows + (a.R < a.E ? a.R : a.E)) * static_cast<long>((a.N + BN - 1) / BN);
 }
 
-template <class T, int WK, int CH, int OUT>
+template <class T, bool SLOTS, int WK, int CH, int OUT>
 hipError_t launch_stream_chunks(const MoeGemmArgs &a, hipStream_t stream)
 {
     const long most = stream_passes<OUT>(a, WK), room = device_cu_count() * (CH <= 2 ? 2 : 1);
-    hipLaunchKernelGGL((moe_stream_kernel<T, WK, CH, OUT>), dim3(most < room ? most : room), dim3(kStreamThreads), 0,
+    hipLaunchKernelGGL((moe_stream_kernel<T, SLOTS, WK, CH, OUT>), dim3(most < room ? most : room), dim3(kStreamThreads), 0,
                        stream, a);
     return hipGetLastError();
 }
 
-// hipErrorNotSupported where the tiles of moe_gemm.hip are faster or K is too
-// long for a wave's registers.
-template <class T, int OUT>
+// Whether a reduction fits the waves' registers.
+inline bool stream_fits(int K)
+{
+    return K >= 64 && K <= kStreamMostChunks * kStreamWaves * kStreamChunk;
+}
+
+template <class T, bool SLOTS, int OUT>
 hipError_t launch_moe_stream(const MoeGemmArgs &a, hipStream_t stream)
 {
-    if (a.R > 16 * a.E || a.K < 64)
-        return hipErrorNotSupported;
     switch ((a.K + kStreamWaves * kStreamChunk - 1) / (kStreamWaves * kStreamChunk)) {
     case 1:
         if (a.K > 512 && stream_passes<OUT>(a, 4) >= 4 * device_cu_count())
-            return launch_stream_chunks<T, 4, 2, OUT>(a, stream);
-        return launch_stream_chunks<T, 8, 1, OUT>(a, stream);
+            return launch_stream_chunks<T, SLOTS, 4, 2, OUT>(a, stream);
+        return launch_stream_chunks<T, SLOTS, 8, 1, OUT>(a, stream);
     case 2:
-        return launch_stream_chunks<T, 8, 2, OUT>(a, stream);
+        return launch_stream_chunks<T, SLOTS, 8, 2, OUT>(a, stream);
     case 3:
-        return launch_stream_chunks<T, 8, 3, OUT>(a, stream);
+        return launch_stream_chunks<T, SLOTS, 8, 3, OUT>(a, stream);
     case 4:
-        return launch_stream_chunks<T, 8, 4, OUT>(a, stream);
+        return launch_stream_chunks<T, SLOTS, 8, 4, OUT>(a, stream);
     case 5:
-        return launch_stream_chunks<T, 8, 5, OUT>(a, stream);
-    case 6:
-        return launch_stream_chunks<T, 8, 6, OUT>(a, stream);
+        return launch_stream_chunks<T, SLOTS, 8, 5, OUT>(a, stream);
     default:
-        return hipErrorNotSupported;
+        return launch_stream_chunks<T, SLOTS, 8, 6, OUT>(a, stream);
     }
 }
 
