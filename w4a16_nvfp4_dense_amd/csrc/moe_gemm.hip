@@ -318,7 +318,7 @@ hipError_t launch_tiles(const MoeGemmArgs &a, hipStream_t stream)
 template <class T, int OUT>
 hipError_t launch_out(const MoeGemmArgs &a, hipStream_t stream)
 {
-    if (a.R <= kStreamRows * a.E && stream_fits(a.K))
+    if (a.R <= kStreamRows * a.E && stream_fits(a.E, a.K, a.N))
         return launch_moe_stream<T, false, OUT>(a, stream);
     const int mean = a.R / a.E;  // rows of an expert
     if (mean > 64)
@@ -356,7 +356,7 @@ hipError_t launch_type(const MoeGemmArgs &a, MoeOut out, hipStream_t stream)
 
 bool moe_by_slots(int R, int E, int K, int N)
 {
-    return R <= kStreamSlots && R <= kStreamRows * E && stream_fits(K) && stream_fits(N);
+    return R <= kStreamSlots && R <= kStreamRows * E && stream_fits(E, K, N) && stream_fits(E, N, K);
 }
 
 hipError_t launch_moe_gemm(const MoeGemmArgs &a, int dtype, MoeOut out, hipStream_t stream)

@@ -68,14 +68,19 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     constexpr int GROUPS = kStreamWaves / WK;
     constexpr int GN = TWO ? 16 : 32;   // channels of a group
     constexpr int BN = GN * GROUPS;     // and of a pass
+    constexpr int FRAGS = 2 * GROUPS;   // fragments of 16 weight rows of a pass
+    constexpr int BLOCK = CH * WK * kStreamChunk;  // most bytes of a fragment's scales: the most columns
+    constexpr int SLOTS_EACH = BLOCK / 1024;       // 64 pieces of 16 bytes each
+    constexpr int PIECES = (FRAGS * SLOTS_EACH + kStreamWaves - 1) / kStreamWaves;  // of a thread
+    static_assert(BLOCK % 1024 == 0, "whole waves");
     typedef typename Half<T>::vec8 vec8;
 
-    __shared__ int begins[kMoeMostExperts + 1];  // where the experts' rows begin
-    __shared__ int ends[kMoeMostExperts];
+    __shared__ int bound[kMoeMostExperts + 1];  // where the experts' rows begin; SLOTS: how many they are
     __shared__ int slot_ids[SLOTS ? kStreamSlots : 1];
     __shared__ int tile_slots[SLOTS ? kStreamWaves : 1][kStreamRows];  // the tile's, for each wave
     __shared__ int wave_sum[kStreamWaves];
     __shared__ int start[2];  // expert and tile of it that the run begins with
+    __shared__ __attribute__((aligned(16))) uint8_t scales_lds[2][FRAGS * BLOCK];  // pass parity
     __shared__ f32x4_t part[2][2][kStreamWaves][64];  // partial sums: pass parity, fragment, wave, lane
 
     const int lane = threadIdx.x & 63;
@@ -90,31 +95,25 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     // This workgroup's run of passes.
     int mine = 0;
     if constexpr (SLOTS) {
-        // (begins is all zero, ends the number of slots)
         for (int e = threadIdx.x; e < a.E; e += kStreamThreads)
-            begins[e] = ends[e] = 0;
+            bound[e] = 0;
         const int id = static_cast<int>(threadIdx.x) < a.R ? a.ids[threadIdx.x] : -1;
         slot_ids[threadIdx.x] = id;
         __syncthreads();
         if (id >= 0 && id < a.E)
-            atomicAdd(&ends[id], 1);
-        __syncthreads();
+            atomicAdd(&bound[id], 1);
+    } else {
+        for (int e = threadIdx.x; e <= a.E; e += kStreamThreads)
+            bound[e] = min(max(a.offsets[e], 0), a.R);
     }
+    __syncthreads();
+    const auto begin_of = [&](int e) { return SLOTS ? 0 : bound[e]; };
+    const auto end_of = [&](int e) { return SLOTS ? bound[e] : max(bound[e + 1], bound[e]); };
+    const auto tiles_of = [&](int e) { return (end_of(e) - begin_of(e) + kStreamRows - 1) / kStreamRows; };
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int e = 2 * threadIdx.x + i;
-        if (e < a.E) {
-            int b = 0, n;
-            if constexpr (SLOTS) {
-                n = ends[e];
-            } else {
-                rows_of(a, e, b, n);
-                begins[e] = b;
-                ends[e] = n;
-            }
-            mine += (n - b + kStreamRows - 1) / kStreamRows;
-        }
-    }
+    for (int i = 0; i < 2; ++i)
+        if (2 * static_cast<int>(threadIdx.x) + i < a.E)
+            mine += tiles_of(2 * threadIdx.x + i);
     int total;
     const int before = stream_tiles_before(mine, wave_sum, total);
     const unsigned all = static_cast<unsigned>(total) * passes;  // (below 2^31: see the launcher)
@@ -126,9 +125,8 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     const int first = static_cast<int>(from / passes);  // the run's first tile
     if (first >= before && first < before + mine) {
         int e = 2 * threadIdx.x, t = first - before;
-        const int tiles = (ends[e] - begins[e] + kStreamRows - 1) / kStreamRows;
-        if (t >= tiles) {
-            t -= tiles;
+        if (t >= tiles_of(e)) {
+            t -= tiles_of(e);
             ++e;
         }
         start[0] = e;
@@ -136,62 +134,77 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     }
     __syncthreads();
     int e = scalar(start[0]);
-    int row_end = scalar(ends[e]), row0 = scalar(begins[e] + start[1] * kStreamRows);
+    int row_end = scalar(end_of(e)), row0 = scalar(begin_of(e) + start[1] * kStreamRows);
     int pass = scalar(static_cast<int>(from) - first * passes);  // (divisions run on the vector unit)
     int left = count;
 
-    // Chunks go in pairs, so that a lane has 64 consecutive columns of a row with
-    // their four scale bytes: chunks 2 j and 2 j + 1 are its columns 256 (w + WK j)
-    // + 64 q .. + 31 and .. + 63; the last chunk of an odd number is columns 128
-    // (WK (CH - 1) + w) + 32 q .. + 31. Only those of the last pair, or the odd
-    // chunk, may lie past the end.
+    // Chunks go in pairs, so that a lane has 64 consecutive columns of a row and a
+    // wave whole lines of memory: chunks 2 j and 2 j + 1 are its columns 256 (w +
+    // WK j) + 64 q .. + 31 and .. + 63; the last chunk of an odd number is columns
+    // 128 (WK (CH - 1) + w) + 32 q .. + 31.
     constexpr int PAIRS = CH / 2;
-    constexpr int LAST = CH % 2 ? CH - 1 : CH - 2;  // first chunk that may be past the end
-    const int pair0 = wk * 256 + 64 * q;
-    const int last0 = CH % 2 ? (CH - 1) * WK * 128 + wk * 128 + 32 * q : pair0 + (PAIRS - 1) * WK * 256;
     const auto col_of = [&](int i) {
-        return i < LAST ? pair0 + (i / 2) * WK * 256 + i % 2 * 32 : last0 + (i - LAST) * 32;
+        return i < 2 * PAIRS ? (wk + i / 2 * WK) * 256 + 64 * q + i % 2 * 32 : (wk + i * WK) * 128 + 32 * q;
     };
 
     // The weight rows of a pass in registers: 32 columns of one row for each
-    // fragment and chunk, two chunks' scales in a register. They are loaded by
-    // buffer, whose bounds check gives zeros for rows past the last channel (and
-    // for the pass behind the run's last, of no rows: the same number of loads
-    // on every path, so that the compiler's waits for the pass at hand are not
-    // waits for the next one); columns past the end have an offset past any
-    // buffer. Of a pair whose second chunk is past the end, the scales are
-    // loaded two bytes earlier, so as to end with the row, and shifted.
+    // fragment and chunk. They are loaded by buffer, whose bounds check gives
+    // zeros for rows past the last channel (and for the pass behind the run's
+    // last, of no rows: the same number of loads on every path, so that the
+    // compiler's waits for the pass at hand are not waits for the next one);
+    // columns past the end have an offset past any buffer.
     struct Rows {
         u32x4_t codes[2][CH];
-        uint32_t scales[2][(CH + 1) / 2];
     };
     const int row_codes = K / 2, row_scales = K / 16;
-    const bool half = CH % 2 == 0 && last0 < K && last0 + 32 >= K;
-    int code_at[CH], scale_at[(CH + 1) / 2];
+    int code_at[CH], scale_at[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         code_at[i] = col_of(i) < K ? r * row_codes + col_of(i) / 2 : kPast;
-        if (i % 2 == 0)
-            scale_at[i / 2] = col_of(i) < K ? r * row_scales + col_of(i) / 16 - (i == LAST && half ? 2 : 0) : kPast;
+        scale_at[i] = group * 2 * BLOCK + (col_of(i) < K ? r * row_scales + col_of(i) / 16 : 0);
     }
+    // The block scales of a fragment are K consecutive bytes, 16 of them for each
+    // thread; they come to LDS by way of registers. (Each lane loading those of
+    // its own chunks touches many lines for a few bytes each, and the lines that
+    // a compute unit can wait for at once are what bounds this: PLACEHOLDER.)
+    u32x4_t piece[PIECES];
+    const auto slot_of = [&](int j) { return j * kStreamWaves + wave; };  // of 64 pieces
+    const auto piece_at = [&](int j) { return slot_of(j) % SLOTS_EACH * 1024 + lane * 16; };
+    // The bounds check is made for each four bytes. Where a block's are two more
+    // than a multiple of four (an odd number of rows, K not a multiple of 64), it
+    // is taken with the two bytes before it (the first of all, with the two behind).
+    const auto rows_from = [&](int n) { return min(max(N - n, 0), 16); };
+    const auto extra_of = [&](int n) { return rows_from(n) * row_scales & 2; };
+    const auto skew_of = [&](int expert, int n) { return expert == 0 && n == 0 ? 0 : extra_of(n); };
     const auto load = [&](Rows &w, int expert, int p, bool real) {
+        const auto block = [&](const uint8_t *m, int n, int row_bytes, int extra) {  // 16 rows from channel n on
+            const size_t row = static_cast<size_t>(scalar(expert)) * N + n;
+            return uniform_buffer(m + row * row_bytes, real ? rows_from(n) * row_bytes + extra : 0);
+        };
+        const int n0 = scalar(p) * BN;
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const int fr = slot_of(j) / SLOTS_EACH, f = fr % 2, n = n0 + fr / 2 * GN + (TWO ? 0 : 16 * f);
+            const auto scales = block((TWO && f == 1 ? a.w1.scales : a.w0.scales) - skew_of(expert, n), n, row_scales,
+                                      extra_of(n));
+            const int at = piece_at(j);
+            piece[j] = __builtin_amdgcn_raw_buffer_load_b128(scales, fr < FRAGS && at < K ? at : kPast, 0, 0);
+        }
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            const int n = scalar(p) * BN + group * GN + (TWO ? 0 : 16 * f);
-            const size_t row = static_cast<size_t>(scalar(expert)) * N + n;
-            const int rows = real ? min(max(N - n, 0), 16) : 0;
-            const auto codes = uniform_buffer((TWO && f == 1 ? a.w1.codes : a.w0.codes) + row * row_codes, rows * row_codes);
-            const auto scales =
-                uniform_buffer((TWO && f == 1 ? a.w1.scales : a.w0.scales) + row * row_scales, rows * row_scales);
+            const auto codes = block(TWO && f == 1 ? a.w1.codes : a.w0.codes,
+                                     n0 + group * GN + (TWO ? 0 : 16 * f), row_codes, 0);
 #pragma unroll
             for (int i = 0; i < CH; ++i)
                 w.codes[f][i] = __builtin_amdgcn_raw_buffer_load_b128(codes, code_at[i], 0, 0);
-#pragma unroll
-            for (int j = 0; j < (CH + 1) / 2; ++j)
-                w.scales[f][j] = 2 * j + 1 == CH ? __builtin_amdgcn_raw_buffer_load_b16(scales, scale_at[j], 0, 0)
-                                                 : __builtin_amdgcn_raw_buffer_load_b32(scales, scale_at[j], 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);  // (nothing that waits for earlier loads goes before these)
+    };
+    const auto keep_scales = [&](int to) {
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j)
+            if (slot_of(j) < FRAGS * SLOTS_EACH)
+                *reinterpret_cast<u32x4_t *>(scales_lds[to] + slot_of(j) * 1024 + lane * 16) = piece[j];
     };
     vec8 x[CH][4];
     float s0 = 0.0f, s1 = 0.0f;
@@ -236,24 +249,27 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
         next_row0 += kStreamRows;
         while (next_row0 >= next_end && next_e + 1 < a.E) {
             ++next_e;
-            next_row0 = scalar(begins[next_e]);
-            next_end = scalar(ends[next_e]);
+            next_row0 = scalar(begin_of(next_e));
+            next_end = scalar(end_of(next_e));
         }
     };
     int parity = 0;
     const auto multiply = [&](const Rows &w) {
         f32x4_t acc[2] = {};
 #pragma unroll
-        for (int f = 0; f < 2; ++f)  // (in the order of their loads)
+        for (int f = 0; f < 2; ++f) {  // (in the order of their loads)
+            const int skew = scalar(skew_of(e, pass * BN + group * GN + (TWO ? 0 : 16 * f)));
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                const uint32_t both = i >= LAST && half ? w.scales[f][i / 2] >> 16 : w.scales[f][i / 2];
-                const float sc0 = i % 2 ? e4m3_to_f32<2>(both) : e4m3_to_f32<0>(both);
-                const float sc1 = i % 2 ? e4m3_to_f32<3>(both) : e4m3_to_f32<1>(both);
+                uint32_t both = *reinterpret_cast<const uint16_t *>(scales_lds[parity] + f * BLOCK + skew + scale_at[i]);
+                if (i >= CH - 2 && col_of(i) >= K)  // (codes are zeros: a scale of NaN would not be)
+                    both = 0;
+                const float sc0 = e4m3_to_f32<0>(both), sc1 = e4m3_to_f32<1>(both);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     acc[f] = Half<T>::mfma(x[i][t], Half<T>::weights(w.codes[f][i][t], t < 2 ? sc0 : sc1), acc[f]);
             }
+        }
 #pragma unroll
         for (int f = 0; f < 2; ++f)
             part[parity][f][wave][lane] = acc[f];
@@ -287,10 +303,13 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
     Rows even, odd;
     load(even, e, pass, true);
     load_tile();
+    keep_scales(0);
+    lds_barrier();
     const auto step = [&](Rows &now, Rows &next) {
         find_next();
         load(next, next_e, next_pass, left > 1);
         multiply(now);
+        keep_scales(parity ^ 1);
         finish();
         const bool tile = next_pass == 0;
         e = next_e;
@@ -328,10 +347,11 @@ hipError_t launch_stream_chunks(const MoeGemmArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Whether a reduction fits the waves' registers.
-inline bool stream_fits(int K)
+// Whether a reduction fits the waves' registers (and the weights have two bytes
+// of scales before or behind any block of rows).
+inline bool stream_fits(int E, int K, int N)
 {
-    return K >= 64 && K <= kStreamMostChunks * kStreamWaves * kStreamChunk;
+    return K <= kStreamMostChunks * kStreamWaves * kStreamChunk && (E > 1 || N >= 16 || K % 64 == 0 || N % 2 == 0);
 }
 
 template <class T, bool SLOTS, int OUT>
