@@ -87,6 +87,17 @@ __device__ __forceinline__ V load_global(uintptr_t at)
     return *(const __attribute__((address_space(1))) V *)at;
 }
 
+// Lanes 32 .. 63 of lo and lanes 0 .. 31 of hi change places.
+__device__ __forceinline__ void swap_halves(uint32_t &lo, uint32_t &hi)
+{
+    const auto both = __builtin_amdgcn_permlane32_swap(lo, hi, false, false);
+    lo = both[0];
+    hi = both[1];
+}
+
+// A byte offset past any buffer.
+constexpr uint32_t kPast = 0xE0000000u;
+
 // A buffer whose base and size are the same in all lanes, which the compiler
 // does not always see.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_buffer(const void *base, int bytes)

@@ -14,16 +14,17 @@
 // XCDs in runs, so that an XCD's L2 holds what its tiles share.
 //
 // A workgroup has four waves; each dequantises 64 weight rows of the tile (32
-// of either weight) and multiplies them with all its rows.
-// Columns go by stages of 128 (weights) in two units of 64 (activations). In
-// stage s, unit v and step t (of four), lane half h = lane / 32 holds columns
-// 128 s + 64 h + 32 v + 8 t .. + 7 of either operand: a lane's weights of a
-// stage are then 64 consecutive columns with four scale bytes.
+// of either weight) and multiplies them with all its rows. Columns go by units
+// of 64; in step t (of four) of a unit, lane half h = lane / 32 holds columns
+// 32 h + 8 t .. + 7 of either operand.
 //
-// Activations and codes come through LDS by direct loads of 16 bytes a lane,
-// two units and two stages deep, the 16-byte pieces swizzled so that reads meet
-// no bank twice; scales come in registers, a stage ahead.
+// Activations and codes come through a ring of LDS stages of one unit each, by
+// direct loads of 16 bytes a lane, the 16-byte pieces swizzled so that reads meet
+// no bank twice; the two scale bytes that a lane needs of a unit come to
+// registers, as long ahead. One barrier a unit.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "kernels.h"
 #include "moe.h"
@@ -108,117 +109,161 @@ __device__ __forceinline__ Tile find_tile(const MoeGemmArgs &a, int nts, int *no
     return t;
 }
 
+// How deep a tile's loads run ahead: units of activations (LDS) and stages of
+// weights (registers).
 template <int MT>
-constexpr int unit_bytes()
+constexpr int units_ahead()
 {
-    return MT * 4096;  // activations of a unit
+    return MT == 4 ? 4 : 8;
 }
-constexpr int kStageBytes = 256 * 64;  // codes of a stage
 template <int MT>
+constexpr int stages_ahead()
+{
+    return MT == 4 ? 2 : 4;
+}
+// On the way out: bytes of a row of results in LDS, and how many fragments of rows
+// go at once.
+template <int OUT>
+constexpr int out_row_bytes()
+{
+    return (moe_two_weights(OUT) ? 128 : 256) * (OUT == MOE_F32 ? 4 : 2) + 16;
+}
+template <int MT, int OUT>
+constexpr int out_pass()
+{
+    return OUT == MOE_F32 && MT == 4 ? 2 : MT;
+}
+// Bytes of LDS, the last 32 of them what find_tile notes.
+template <int MT, int OUT>
 constexpr int tile_lds()
 {
-    return 2 * unit_bytes<MT>() + 2 * kStageBytes + 32;
+    constexpr int ring = units_ahead<MT>() * MT * 4096, out = 32 * out_pass<MT, OUT>() * out_row_bytes<OUT>();
+    return (ring > out ? ring : out) + 32;
 }
 
-template <class T, int MT, int OUT>
+// WIDE: x does not fit a buffer of 32-bit offsets.
+template <class T, int MT, int OUT, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs a)
 {
     constexpr bool TWO = moe_two_weights(OUT);
     constexpr int BM = 32 * MT;
-    constexpr int WR = TWO ? 32 : 64;     // channels of a wave
+    constexpr int WR = TWO ? 32 : 64;  // channels of a wave
     constexpr int BN = 4 * WR;
+    constexpr int S = units_ahead<MT>(), D = stages_ahead<MT>(), UNIT = MT * 4096;
     typedef typename Half<T>::vec8 vec8;
-    constexpr int LOADS_W = 4;            // direct loads of a stage's codes, for each wave
 
     extern __shared__ u32x4_t lds_raw[];
     FFN_LDS uint8_t *lds = (FFN_LDS uint8_t *)lds_raw;
-    constexpr int XRING = 2 * unit_bytes<MT>();
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = lane >> 5, r = lane & 31;
     const int K = a.K, N = a.N;
-    const Tile tile = find_tile<BM>(a, (N + BN - 1) / BN,
-                                    reinterpret_cast<int *>(reinterpret_cast<char *>(lds_raw) + XRING + 2 * kStageBytes));
+    const Tile tile =
+        find_tile<BM>(a, (N + BN - 1) / BN, reinterpret_cast<int *>(reinterpret_cast<char *>(lds_raw) + tile_lds<MT, OUT>() - 32));
     if (tile.e < 0)
         return;
 
+    // Whatever is past an end (rows of the tile, channels, columns, stages) is
+    // loaded with an offset past its buffer, which gives zeros.
+    const int whole = K / kStageCols, stages = (K + kStageCols - 1) / kStageCols;
+    const int rest = K - whole * kStageCols;  // columns of a last stage that is not whole
     // This lane's 16-byte pieces of the activations: piece P = 64 i + lane of
-    // the wave's, of row P / 8 of the tile, piece (P % 8) ^ (row / 2 % 8) of a
-    // unit, which are columns 64 (piece / 4) + 8 (piece % 4) of it.
-    const T *xp[MT];
-    int xcol[MT];
+    // the wave's, of row P / 8 of the tile, piece c = (P % 8) ^ (row / 2 % 8) of a
+    // unit: columns 64 (c / 4) + 8 (c % 4) of a stage, 32 further on in its second unit.
+    uint32_t x_at[MT];
+    int x_col[MT];
+    const T *x_from[WIDE ? MT : 1];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int m = (wave * MT + i) * 8 + (lane >> 3);
         const int c = (lane & 7) ^ ((m >> 1) & 7);
-        int row = min(tile.begin + m, tile.end - 1);
-        if (a.rows)
-            row = min(max(a.rows[row], 0) / a.top_k, a.x_rows - 1);
-        xcol[i] = 64 * (c >> 2) + 8 * (c & 3);
-        xp[i] = static_cast<const T *>(a.x) + static_cast<size_t>(row) * K + xcol[i];
+        const bool there = tile.begin + m < tile.end;
+        const int row = !there ? 0 : a.rows ? min(max(a.rows[tile.begin + m], 0) / a.top_k, a.x_rows - 1) : m;
+        x_col[i] = 64 * (c >> 2) + 8 * (c & 3);
+        x_at[i] = there ? static_cast<uint32_t>(row) * (2 * K) + 2 * x_col[i] : kPast;
+        if constexpr (WIDE)
+            x_from[i] = there ? static_cast<const T *>(a.x) + static_cast<size_t>(row) * K + x_col[i] : nullptr;
     }
-    // Its pieces of the codes: piece j of four, of row 16 j + lane / 4 of the
-    // wave's 64, columns 32 ((lane % 4) ^ (row / 4 % 4)) .. of a stage.
-    const size_t row_codes = static_cast<size_t>(K) / 2, row_scales = static_cast<size_t>(K) / 16;
-    const size_t expert = static_cast<size_t>(tile.e) * N;
-    const auto channel = [&](int i) {  // of weight row i of the wave
-        return min(tile.nt * BN + wave * WR + (TWO ? i & 31 : i), N - 1);
+    const T *x_base = static_cast<const T *>(a.x) + (a.rows ? size_t{0} : static_cast<size_t>(tile.begin) * K);
+    const auto x_buffer =
+        uniform_buffer(x_base, a.rows ? static_cast<int>(static_cast<uint32_t>(a.x_rows) * (2 * K)) : 2 * BM * K);
+    const auto direct = [&](const __amdgpu_buffer_rsrc_t &from, int to, uint32_t at, int offset) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, reinterpret_cast<FFN_LDS void *>(lds + to), 16, at, offset, 0, 0);
     };
-    const uint8_t *wp[4];
-    int wcol[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int i = 16 * j + (lane >> 2);
-        const int c = (lane & 3) ^ ((i >> 2) & 3);
-        const uint8_t *codes = TWO && j >= 2 ? a.w1.codes : a.w0.codes;
-        wcol[j] = 32 * c;
-        wp[j] = codes + (expert + channel(i)) * row_codes + 16 * c;
-    }
-    const uint8_t *sp[2];
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-        const uint8_t *scales = TWO && f == 1 ? a.w1.scales : a.w0.scales;
-        sp[f] = scales + (expert + channel(32 * f + r)) * row_scales + 4 * h;
-    }
-
-    // Of a last stage of fewer columns, pieces past the end are loaded from zeros.
-    const auto load_x = [&](int s, int v) {
-        FFN_LDS uint8_t *to = lds + v * unit_bytes<MT>() + wave * MT * 1024;
-        const int k0 = s * kStageCols + v * 32;
-        const bool whole = (s + 1) * kStageCols <= K;
+    const auto load_x = [&](int s, int v, int slot) {
+        const int to = slot * UNIT + wave * MT * 1024;
+        const int most = (s < whole ? kStageCols : s < stages ? rest : 0) - v * 32;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const void *from = xp[i] + k0;
-            if (!whole && k0 + xcol[i] >= K)
-                from = &kZeros;
-            __builtin_amdgcn_global_load_lds(from, reinterpret_cast<FFN_LDS void *>(to + i * 1024), 16, 0, 0);
-        }
-    };
-    uint32_t scale_next[2];
-    const auto load_w = [&](int s) {
-        FFN_LDS uint8_t *to = lds + XRING + (s & 1) * kStageBytes + wave * 4096;
-        const int k0 = s * kStageCols;
-        const bool whole = k0 + kStageCols <= K;
-        if (whole) {
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-                scale_next[f] = reinterpret_cast<const pair16_t *>(sp[f] + s * 8)->both;
-        } else {
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const uint16_t *p = reinterpret_cast<const uint16_t *>(sp[f] + s * 8);
-                const uint32_t lo = k0 + 64 * h < K ? p[0] : 0, hi = k0 + 64 * h + 32 < K ? p[1] : 0;
-                scale_next[f] = lo | hi << 16;
+            const bool there = x_col[i] < most;
+            if constexpr (WIDE) {
+                const uintptr_t from = there && x_from[i] ? reinterpret_cast<uintptr_t>(x_from[i] + s * kStageCols + v * 32)
+                                                          : reinterpret_cast<uintptr_t>(&kZeros);
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                                 reinterpret_cast<FFN_LDS void *>(lds + to + i * 1024), 16, 0, 0);
+            } else {
+                direct(x_buffer, to + i * 1024, there ? x_at[i] : kPast, s * 256 + v * 64);
             }
         }
+    };
+    // The weights: lane (h, r) holds columns 64 h + 32 v .. + 31 of a stage's unit
+    // v, of row r of a fragment. Its four scale bytes of a stage come with those
+    // of three more: lane (h, r) loads bytes 16 h .. + 15 of a row's 32, and the
+    // halves of the wave swap what is the other's.
+    const int row_codes = K / 2, row_scales = K / 16;
+    const int n0 = tile.nt * BN + wave * WR;  // the wave's first channel
+    const auto rows_of_weight = [&](const uint8_t *m, int first, int row_bytes) {
+        return uniform_buffer(m + (static_cast<size_t>(tile.e) * N + first) * row_bytes,
+                              min(max(N - first, 0), 32) * row_bytes);
+    };
+    __amdgpu_buffer_rsrc_t codes[2], scales[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const void *from = wp[j] + k0 / 2;
-            if (!whole && k0 + wcol[j] >= K)
-                from = &kZeros;
-            __builtin_amdgcn_global_load_lds(from, reinterpret_cast<FFN_LDS void *>(to + j * 1024), 16, 0, 0);
+    for (int f = 0; f < 2; ++f) {
+        const int first = n0 + (TWO ? 0 : 32 * f);
+        codes[f] = rows_of_weight(TWO && f == 1 ? a.w1.codes : a.w0.codes, first, row_codes);
+        scales[f] = rows_of_weight(TWO && f == 1 ? a.w1.scales : a.w0.scales, first, row_scales);
+    }
+    const uint32_t code_at = r * row_codes + 32 * h, scale_at = r * row_scales + 16 * h;
+    u32x4_t code[D][2][2];  // stage, fragment, unit
+    const auto load_w = [&](int s, int slot) {
+        const int most = (s < whole ? kStageCols : s < stages ? rest : 0) - 64 * h;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const uint32_t at = 32 * v < most ? code_at + 16 * v : kPast;
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+                code[slot][f][v] = __builtin_amdgcn_raw_buffer_load_b128(codes[f], at, s * 64, 0);
         }
     };
+    u32x4_t scale[2], scale_next[2];  // of four stages
+    const auto load_scales = [&](int s) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+            scale_next[f] = __builtin_amdgcn_raw_buffer_load_b128(scales[f], scale_at, s * 8, 0);
+    };
+    const auto take_scales = [&]() {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t lo = scale_next[f][2 * i], hi = scale_next[f][2 * i + 1];
+                swap_halves(lo, hi);
+                scale[f][i] = lo;
+                scale[f][2 + i] = hi;
+            }
+    };
+    // Those of a last stage that is not whole: the bounds check, made for each four
+    // bytes, would drop the last two of an odd number of rows.
+    uint32_t last_scale[2] = {0, 0};
+    if (rest) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const uint32_t at = r * row_scales + whole * 8 + 4 * h;
+            const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(scales[f], 64 * h < rest ? at : kPast, 0, 0);
+            const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(scales[f], 64 * h + 32 < rest ? at + 2 : kPast, 0, 0);
+            last_scale[f] = lo | hi << 16;
+        }
+    }
 
     f32x16_t acc[2][MT];
 #pragma unroll
@@ -226,28 +271,24 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
             acc[f][mt] = f32x16_t{};
-    uint32_t scale[2];
-    const auto multiply = [&](int s, int v) {
-        const FFN_LDS uint8_t *codes = lds + XRING + (s & 1) * kStageBytes + wave * 4096;
-        const FFN_LDS uint8_t *x = lds + v * unit_bytes<MT>();
-        u32x4_t q[2];
-        float sc[2][2];
+    // A unit's products, of the first R fragments of rows.
+    const auto multiply = [&](auto fragments, int v, int slot, const u32x4_t (&q)[2][2], const uint32_t (&sc)[2]) {
+        constexpr int R = decltype(fragments)::value;
+        const FFN_LDS uint8_t *x = lds + slot * UNIT;
+        float s[2][2];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            const int i = 32 * f + r;
-            q[f] = *reinterpret_cast<const FFN_LDS u32x4_t *>(codes + i * 64 + (((2 * h + v) ^ ((i >> 2) & 3)) * 16));
-            const uint32_t two = scale[f] >> (16 * v);
-            sc[f][0] = e4m3_to_f32<0>(two);
-            sc[f][1] = e4m3_to_f32<1>(two);
+            s[f][0] = v ? e4m3_to_f32<2>(sc[f]) : e4m3_to_f32<0>(sc[f]);
+            s[f][1] = v ? e4m3_to_f32<3>(sc[f]) : e4m3_to_f32<1>(sc[f]);
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             vec8 w[2];
 #pragma unroll
             for (int f = 0; f < 2; ++f)
-                w[f] = Half<T>::weights(q[f][t], sc[f][t >> 1]);
+                w[f] = Half<T>::weights(q[f][v][t], s[f][t >> 1]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+            for (int mt = 0; mt < R; ++mt) {
                 const int m = 32 * mt + r;
                 const vec8 xv = *reinterpret_cast<const FFN_LDS vec8 *>(x + m * 128 + (((4 * h + t) ^ ((m >> 1) & 7)) * 16));
                 acc[0][mt] = Half<T>::mfma(xv, w[0], acc[0][mt]);
@@ -256,62 +297,109 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
         }
     };
 
-    const int stages = (K + kStageCols - 1) / kStageCols;
-    load_w(0);
-    load_x(0, 0);
-    for (int s = 0; s < stages; ++s) {
-        wait_vmcnt<0>();
-        lds_barrier();
-        scale[0] = scale_next[0];
-        scale[1] = scale_next[1];
-        load_x(s, 1);
-        if (s + 1 < stages)
-            load_w(s + 1);
-        multiply(s, 0);
-        if (s + 1 < stages)
-            wait_vmcnt<LOADS_W>();
-        else
-            wait_vmcnt<0>();
-        lds_barrier();
-        if (s + 1 < stages)
-            load_x(s + 1, 0);
-        multiply(s, 1);
-    }
-
-    // Value 4 g + c of acc[f][mt]: row 32 mt + 8 g + 4 h + c, weight row r of
-    // fragment f.
-    const float s0 = a.w0.scale2[tile.e], s1 = TWO ? a.w1.scale2[tile.e] : s0;
-    const int n0 = tile.nt * BN + wave * WR + r;
+    const auto run = [&](auto fragments) {
+        load_scales(0);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-            const int i = tile.begin + 32 * mt + 8 * (v >> 2) + 4 * h + (v & 3);
-            if (i >= tile.end)
-                continue;
-            const float y0 = acc[0][mt][v], y1 = acc[1][mt][v];
-            const size_t o = static_cast<size_t>(i) * N + n0;
-            if (n0 < N)
-                moe_store<T, OUT>(a.out, o, moe_value<OUT>(y0, y1, s0, s1));
-            if (!TWO && n0 + 32 < N)
-                moe_store<T, OUT>(a.out, o + 32, moe_value<OUT>(y1, 0.0f, s0, s1));
+        for (int u = 0; u < S - 1; ++u) {
+            if (u % 2 == 1 && u / 2 < D - 1)
+                load_w(u / 2, u / 2);
+            load_x(u / 2, u % 2, u);
         }
+        static_assert(S == 2 * D && 4 % D == 0, "every round has the rings' places alike");
+        for (int s0 = 0; s0 < stages; s0 += 4) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int s = s0 + u / 2, v = u % 2;
+                if (v == 0 && s >= stages)
+                    break;
+                // This unit's activations have landed here once at most the loads
+                // of the S - 2 units after them are in flight (and the weights of
+                // every other one), and in every wave behind the barrier, where
+                // all are done with the unit before.
+                wait_vmcnt<(S - 2) * MT + (S - 2) / 2 * 4>();
+                lds_barrier();
+                if (u == 0) {
+                    take_scales();
+                    load_scales(s + 4);
+                }
+                if (v == 0)
+                    load_w(s + D - 1, (u / 2 + D - 1) % D);
+                const int next = u + S - 1;
+                load_x(s0 + next / 2, next % 2, next % S);
+                __builtin_amdgcn_sched_barrier(0);  // (loads first, then what waits)
+                uint32_t sc[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    sc[f] = s < whole ? scale[f][u / 2] : last_scale[f];
+                multiply(fragments, v, u % S, code[(u / 2) % D], sc);
+            }
+        }
+    };
+    // A tile of fewer rows takes as many products as it needs.
+    const int rows = tile.end - tile.begin;
+    if (MT >= 2 && rows <= 32)
+        run(std::integral_constant<int, 1>{});
+    else if (MT >= 4 && rows <= 64)
+        run(std::integral_constant<int, (MT >= 4 ? 2 : 1)>{});
+    else
+        run(std::integral_constant<int, MT>{});
+
+    // Results go through LDS, so that the channels of a row leave as whole lines
+    // (two bytes a lane straight from the accumulators: 15 - 28 us a tile for
+    // 2 - 4). Value 4 g + c of acc[f][mt] is row 32 mt + 8 g + 4 h + c, weight row r
+    // of fragment f. The padding of a row keeps both halves of a wave apart.
+    typedef typename std::conditional<OUT == MOE_F32, float, T>::type Out;
+    constexpr int PASS = out_pass<MT, OUT>(), ROW = out_row_bytes<OUT>();
+    constexpr int EACH = 16 / sizeof(Out), PIECES = BN / EACH;  // pieces of 16 bytes of a row
+    const float s0 = a.w0.scale2[tile.e], s1 = TWO ? a.w1.scale2[tile.e] : s0;
+    Out *out = static_cast<Out *>(a.out);
+    wait_vmcnt<0>();  // (also of loads behind the last unit)
+#pragma unroll
+    for (int mt0 = 0; mt0 < MT; mt0 += PASS) {
+        lds_barrier();
+#pragma unroll
+        for (int mt = mt0; mt < mt0 + PASS; ++mt)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int i = 32 * (mt - mt0) + 8 * (v >> 2) + 4 * h + (v & 3);
+                FFN_LDS Out *to = reinterpret_cast<FFN_LDS Out *>(lds + i * ROW) + wave * WR + r;
+                const float y0 = acc[0][mt][v], y1 = acc[1][mt][v];
+                *to = static_cast<Out>(moe_value<OUT>(y0, y1, s0, s1));
+                if constexpr (!TWO)
+                    to[32] = static_cast<Out>(moe_value<OUT>(y1, 0.0f, s0, s1));
+            }
+        lds_barrier();
+        const int first = tile.begin + 32 * mt0, most = min(32 * PASS, tile.end - first);
+        if (N % EACH == 0) {
+            const int n = static_cast<int>(threadIdx.x) % PIECES * EACH, to = tile.nt * BN + n;
+            for (int i = threadIdx.x / PIECES; i < most; i += kThreads / PIECES)
+                if (to < N)
+                    *reinterpret_cast<u32x4_t *>(out + static_cast<size_t>(first + i) * N + to) =
+                        *reinterpret_cast<const FFN_LDS u32x4_t *>(lds + i * ROW + n * sizeof(Out));
+        } else {
+            const int n = static_cast<int>(threadIdx.x) % BN, to = tile.nt * BN + n;
+            for (int i = threadIdx.x / BN; i < most; i += kThreads / BN)
+                if (to < N)
+                    out[static_cast<size_t>(first + i) * N + to] =
+                        reinterpret_cast<const FFN_LDS Out *>(lds + i * ROW)[n];
+        }
+    }
 }
 
-template <class T, int MT, int OUT>
+template <class T, int MT, int OUT, bool WIDE = false>
 hipError_t launch_tiles(const MoeGemmArgs &a, hipStream_t stream)
 {
-    constexpr int BM = 32 * MT, BN = moe_two_weights(OUT) ? 128 : 256;
-    auto kern = moe_tile_kernel<T, MT, OUT>;
+    constexpr int BM = 32 * MT, BN = moe_two_weights(OUT) ? 128 : 256, lds = tile_lds<MT, OUT>();
+    auto kern = moe_tile_kernel<T, MT, OUT, WIDE>;
     static std::atomic<uint64_t> lds_done{0};
-    const hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), tile_lds<MT>(), lds_done);
+    const hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), lds, lds_done);
     if (e != hipSuccess)
         return e;
     // The most tiles of rows that R rows make: every expert with rows may have
     // one that is not full.
     const long most = a.R / BM + (a.R < a.E ? a.R : a.E);
     const long grid = (most * ((a.N + BN - 1) / BN) + 7) / 8 * 8;
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(kThreads), tile_lds<MT>(), stream, a);
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(kThreads), lds, stream, a);
     return hipGetLastError();
 }
 
@@ -320,6 +408,8 @@ hipError_t launch_out(const MoeGemmArgs &a, hipStream_t stream)
 {
     if (a.R <= kStreamRows * a.E && stream_fits(a.E, a.K, a.N))
         return launch_moe_stream<T, false, OUT>(a, stream);
+    if (a.rows && static_cast<uint64_t>(a.x_rows) * a.K * 2 >= kPast)
+        return launch_tiles<T, 2, OUT, true>(a, stream);
     const int mean = a.R / a.E;  // rows of an expert
     if (mean > 64)
         return launch_tiles<T, 4, OUT>(a, stream);

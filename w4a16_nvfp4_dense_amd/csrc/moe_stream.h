@@ -29,7 +29,6 @@ constexpr int kStreamChunk = 128;  // columns of a wave's chunk
 constexpr int kStreamMostChunks = 6;
 constexpr int kStreamSlots = kStreamThreads;  // a thread for each
 constexpr int kMoeMostExperts = 1024;
-constexpr int kPast = 1 << 30;  // a byte offset past any buffer of rows
 
 // Tiles of 16 rows of experts before this thread's (it has experts 2 tid and
 // 2 tid + 1), and of all. Every thread of the workgroup calls it.
@@ -157,7 +156,8 @@ __global__ __launch_bounds__(kStreamThreads, CH <= 2 ? 4 : 2) void moe_stream_ke
         u32x4_t codes[2][CH];
     };
     const int row_codes = K / 2, row_scales = K / 16;
-    int code_at[CH], scale_at[CH];
+    uint32_t code_at[CH];
+    int scale_at[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         code_at[i] = col_of(i) < K ? r * row_codes + col_of(i) / 2 : kPast;
