@@ -1043,8 +1043,9 @@ def _check_moe_weight(w: MoeDeviceWeight, experts: int, rows: int, cols: int, na
 def _check_current(device) -> None:
     """The library launches on the current device, which has to be the tensors'."""
     import torch
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    current = torch.cuda.current_device()
+    if device.index != current:
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{current}")
 
 
 def _moe_half(dtype, name: str) -> int:

@@ -25,7 +25,7 @@ namespace {
 constexpr int kWaves = 16;
 constexpr int kThreads = kWaves * 64;
 constexpr int kMostExperts = 1024;
-constexpr int kChunk = 4096;  // slots of a workgroup, where there are several
+constexpr int kChunk = 2048;  // slots of a workgroup, where there are several
 constexpr int kOnce = 8192;
 
 static_assert(kMostExperts <= kThreads, "a thread for each expert");
@@ -110,6 +110,7 @@ __global__ __launch_bounds__(kThreads) void moe_place_kernel(const int32_t *ids,
     int mine = 0, earlier = 0;  // slots of expert e: all, and those of earlier chunks
     if (e < E) {
         if (counts)
+#pragma unroll 16
             for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
                 const int c = counts[static_cast<size_t>(b) * E + e];
                 mine += c;
