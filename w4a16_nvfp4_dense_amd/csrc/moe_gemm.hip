@@ -121,12 +121,18 @@ constexpr int stages_ahead()
 {
     return MT == 4 ? 2 : 4;
 }
+// Channels of a tile: four waves have NF fragments of 32 weight rows each.
+template <int NF, int OUT>
+constexpr int tile_channels()
+{
+    return moe_two_weights(OUT) ? 128 : 128 * NF;
+}
 // On the way out: bytes of a row of results in LDS, and how many fragments of rows
 // go at once.
-template <int OUT>
+template <int NF, int OUT>
 constexpr int out_row_bytes()
 {
-    return (moe_two_weights(OUT) ? 128 : 256) * (OUT == MOE_F32 ? 4 : 2) + 16;
+    return tile_channels<NF, OUT>() * (OUT == MOE_F32 ? 4 : 2) + 16;
 }
 template <int MT, int OUT>
 constexpr int out_pass()
@@ -134,21 +140,21 @@ constexpr int out_pass()
     return OUT == MOE_F32 && MT == 4 ? 2 : MT;
 }
 // Bytes of LDS, the last 32 of them what find_tile notes.
-template <int MT, int OUT>
+template <int MT, int NF, int OUT>
 constexpr int tile_lds()
 {
-    constexpr int ring = units_ahead<MT>() * MT * 4096, out = 32 * out_pass<MT, OUT>() * out_row_bytes<OUT>();
+    constexpr int ring = units_ahead<MT>() * MT * 4096, out = 32 * out_pass<MT, OUT>() * out_row_bytes<NF, OUT>();
     return (ring > out ? ring : out) + 32;
 }
 
 // WIDE: x does not fit a buffer of 32-bit offsets.
-template <class T, int MT, int OUT, bool WIDE>
+template <class T, int MT, int NF, int OUT, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs a)
 {
     constexpr bool TWO = moe_two_weights(OUT);
     constexpr int BM = 32 * MT;
-    constexpr int WR = TWO ? 32 : 64;  // channels of a wave
-    constexpr int BN = 4 * WR;
+    constexpr int BN = tile_channels<NF, OUT>(), WR = BN / 4;  // channels of the tile and of a wave
+    static_assert(!TWO || NF == 2, "a fragment of either weight");
     constexpr int S = units_ahead<MT>(), D = stages_ahead<MT>(), UNIT = MT * 4096;
     typedef typename Half<T>::vec8 vec8;
 
@@ -159,7 +165,7 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
     const int h = lane >> 5, r = lane & 31;
     const int K = a.K, N = a.N;
     const Tile tile =
-        find_tile<BM>(a, (N + BN - 1) / BN, reinterpret_cast<int *>(reinterpret_cast<char *>(lds_raw) + tile_lds<MT, OUT>() - 32));
+        find_tile<BM>(a, (N + BN - 1) / BN, reinterpret_cast<int *>(reinterpret_cast<char *>(lds_raw) + tile_lds<MT, NF, OUT>() - 32));
     if (tile.e < 0)
         return;
 
@@ -216,34 +222,34 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
         return uniform_buffer(m + (static_cast<size_t>(tile.e) * N + first) * row_bytes,
                               min(max(N - first, 0), 32) * row_bytes);
     };
-    __amdgpu_buffer_rsrc_t codes[2], scales[2];
+    __amdgpu_buffer_rsrc_t codes[NF], scales[NF];
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
+    for (int f = 0; f < NF; ++f) {
         const int first = n0 + (TWO ? 0 : 32 * f);
         codes[f] = rows_of_weight(TWO && f == 1 ? a.w1.codes : a.w0.codes, first, row_codes);
         scales[f] = rows_of_weight(TWO && f == 1 ? a.w1.scales : a.w0.scales, first, row_scales);
     }
     const uint32_t code_at = r * row_codes + 32 * h, scale_at = r * row_scales + 16 * h;
-    u32x4_t code[D][2][2];  // stage, fragment, unit
+    u32x4_t code[D][NF][2];  // stage, fragment, unit
     const auto load_w = [&](int s, int slot) {
         const int most = (s < whole ? kStageCols : s < stages ? rest : 0) - 64 * h;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
             const uint32_t at = 32 * v < most ? code_at + 16 * v : kPast;
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
+            for (int f = 0; f < NF; ++f)
                 code[slot][f][v] = __builtin_amdgcn_raw_buffer_load_b128(codes[f], at, s * 64, 0);
         }
     };
-    u32x4_t scale[2], scale_next[2];  // of four stages
+    u32x4_t scale[NF], scale_next[NF];  // of four stages
     const auto load_scales = [&](int s) {
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+        for (int f = 0; f < NF; ++f)
             scale_next[f] = __builtin_amdgcn_raw_buffer_load_b128(scales[f], scale_at, s * 8, 0);
     };
     const auto take_scales = [&]() {
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+        for (int f = 0; f < NF; ++f)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t lo = scale_next[f][2 * i], hi = scale_next[f][2 * i + 1];
@@ -254,10 +260,10 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
     };
     // Those of a last stage that is not whole: the bounds check, made for each four
     // bytes, would drop the last two of an odd number of rows.
-    uint32_t last_scale[2] = {0, 0};
+    uint32_t last_scale[NF] = {};
     if (rest) {
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
+        for (int f = 0; f < NF; ++f) {
             const uint32_t at = r * row_scales + whole * 8 + 4 * h;
             const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(scales[f], 64 * h < rest ? at : kPast, 0, 0);
             const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(scales[f], 64 * h + 32 < rest ? at + 2 : kPast, 0, 0);
@@ -265,34 +271,35 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
         }
     }
 
-    f32x16_t acc[2][MT];
+    f32x16_t acc[NF][MT];
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < NF; ++f)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
             acc[f][mt] = f32x16_t{};
     // A unit's products, of the first R fragments of rows.
-    const auto multiply = [&](auto fragments, int v, int slot, const u32x4_t (&q)[2][2], const uint32_t (&sc)[2]) {
+    const auto multiply = [&](auto fragments, int v, int slot, const u32x4_t (&q)[NF][2], const uint32_t (&sc)[NF]) {
         constexpr int R = decltype(fragments)::value;
         const FFN_LDS uint8_t *x = lds + slot * UNIT;
-        float s[2][2];
+        float s[NF][2];
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
+        for (int f = 0; f < NF; ++f) {
             s[f][0] = v ? e4m3_to_f32<2>(sc[f]) : e4m3_to_f32<0>(sc[f]);
             s[f][1] = v ? e4m3_to_f32<3>(sc[f]) : e4m3_to_f32<1>(sc[f]);
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            vec8 w[2];
+            vec8 w[NF];
 #pragma unroll
-            for (int f = 0; f < 2; ++f)
+            for (int f = 0; f < NF; ++f)
                 w[f] = Half<T>::weights(q[f][v][t], s[f][t >> 1]);
 #pragma unroll
             for (int mt = 0; mt < R; ++mt) {
                 const int m = 32 * mt + r;
                 const vec8 xv = *reinterpret_cast<const FFN_LDS vec8 *>(x + m * 128 + (((4 * h + t) ^ ((m >> 1) & 7)) * 16));
-                acc[0][mt] = Half<T>::mfma(xv, w[0], acc[0][mt]);
-                acc[1][mt] = Half<T>::mfma(xv, w[1], acc[1][mt]);
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    acc[f][mt] = Half<T>::mfma(xv, w[f], acc[f][mt]);
             }
         }
     };
@@ -316,7 +323,7 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
                 // of the S - 2 units after them are in flight (and the weights of
                 // every other one), and in every wave behind the barrier, where
                 // all are done with the unit before.
-                wait_vmcnt<(S - 2) * MT + (S - 2) / 2 * 4>();
+                wait_vmcnt<(S - 2) * MT + (S - 2) / 2 * 2 * NF>();
                 lds_barrier();
                 if (u == 0) {
                     take_scales();
@@ -327,9 +334,9 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
                 const int next = u + S - 1;
                 load_x(s0 + next / 2, next % 2, next % S);
                 __builtin_amdgcn_sched_barrier(0);  // (loads first, then what waits)
-                uint32_t sc[2];
+                uint32_t sc[NF];
 #pragma unroll
-                for (int f = 0; f < 2; ++f)
+                for (int f = 0; f < NF; ++f)
                     sc[f] = s < whole ? scale[f][u / 2] : last_scale[f];
                 multiply(fragments, v, u % S, code[(u / 2) % D], sc);
             }
@@ -349,7 +356,7 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
     // 2 - 4). Value 4 g + c of acc[f][mt] is row 32 mt + 8 g + 4 h + c, weight row r
     // of fragment f. The padding of a row keeps both halves of a wave apart.
     typedef typename std::conditional<OUT == MOE_F32, float, T>::type Out;
-    constexpr int PASS = out_pass<MT, OUT>(), ROW = out_row_bytes<OUT>();
+    constexpr int PASS = out_pass<MT, OUT>(), ROW = out_row_bytes<NF, OUT>();
     constexpr int EACH = 16 / sizeof(Out), PIECES = BN / EACH;  // pieces of 16 bytes of a row
     const float s0 = a.w0.scale2[tile.e], s1 = TWO ? a.w1.scale2[tile.e] : s0;
     Out *out = static_cast<Out *>(a.out);
@@ -363,9 +370,9 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
             for (int v = 0; v < 16; ++v) {
                 const int i = 32 * (mt - mt0) + 8 * (v >> 2) + 4 * h + (v & 3);
                 FFN_LDS Out *to = reinterpret_cast<FFN_LDS Out *>(lds + i * ROW) + wave * WR + r;
-                const float y0 = acc[0][mt][v], y1 = acc[1][mt][v];
+                const float y0 = acc[0][mt][v], y1 = acc[NF - 1][mt][v];
                 *to = static_cast<Out>(moe_value<OUT>(y0, y1, s0, s1));
-                if constexpr (!TWO)
+                if constexpr (!TWO && NF == 2)
                     to[32] = static_cast<Out>(moe_value<OUT>(y1, 0.0f, s0, s1));
             }
         lds_barrier();
@@ -386,19 +393,23 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
     }
 }
 
-template <class T, int MT, int OUT, bool WIDE = false>
+// The most tiles that R rows make: every expert with rows may have one that is not
+// full.
+inline long most_tiles(const MoeGemmArgs &a, int BM, int BN)
+{
+    return (a.R / BM + static_cast<long>(a.R < a.E ? a.R : a.E)) * ((a.N + BN - 1) / BN);
+}
+
+template <class T, int MT, int NF, int OUT, bool WIDE = false>
 hipError_t launch_tiles(const MoeGemmArgs &a, hipStream_t stream)
 {
-    constexpr int BM = 32 * MT, BN = moe_two_weights(OUT) ? 128 : 256, lds = tile_lds<MT, OUT>();
-    auto kern = moe_tile_kernel<T, MT, OUT, WIDE>;
+    constexpr int BM = 32 * MT, BN = tile_channels<NF, OUT>(), lds = tile_lds<MT, NF, OUT>();
+    auto kern = moe_tile_kernel<T, MT, NF, OUT, WIDE>;
     static std::atomic<uint64_t> lds_done{0};
     const hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), lds, lds_done);
     if (e != hipSuccess)
         return e;
-    // The most tiles of rows that R rows make: every expert with rows may have
-    // one that is not full.
-    const long most = a.R / BM + (a.R < a.E ? a.R : a.E);
-    const long grid = (most * ((a.N + BN - 1) / BN) + 7) / 8 * 8;
+    const long grid = (most_tiles(a, BM, BN) + 7) / 8 * 8;
     hipLaunchKernelGGL(kern, dim3(grid), dim3(kThreads), lds, stream, a);
     return hipGetLastError();
 }
@@ -409,13 +420,17 @@ hipError_t launch_out(const MoeGemmArgs &a, hipStream_t stream)
     if (a.R <= kStreamRows * a.E && stream_fits(a.E, a.K, a.N))
         return launch_moe_stream<T, false, OUT>(a, stream);
     if (a.rows && static_cast<uint64_t>(a.x_rows) * a.K * 2 >= kPast)
-        return launch_tiles<T, 2, OUT, true>(a, stream);
-    const int mean = a.R / a.E;  // rows of an expert
-    if (mean > 64)
-        return launch_tiles<T, 4, OUT>(a, stream);
+        return launch_tiles<T, 2, 2, OUT, true>(a, stream);
+    const int mean = a.R / a.E, cus = device_cu_count();  // rows of an expert
+    constexpr int BN = tile_channels<2, OUT>();
+    if (mean > 64 && most_tiles(a, 128, BN) >= cus)
+        return launch_tiles<T, 4, 2, OUT>(a, stream);
+    if constexpr (!moe_two_weights(OUT))
+        if (mean > 24 && most_tiles(a, 64, BN) < cus)
+            return launch_tiles<T, 2, 1, OUT>(a, stream);
     if (mean > 24)
-        return launch_tiles<T, 2, OUT>(a, stream);
-    return launch_tiles<T, 1, OUT>(a, stream);
+        return launch_tiles<T, 2, 2, OUT>(a, stream);
+    return launch_tiles<T, 1, 2, OUT>(a, stream);
 }
 
 template <class T, int OUT>
