@@ -311,6 +311,7 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
             if (u % 2 == 1 && u / 2 < D - 1)
                 load_w(u / 2, u / 2);
             load_x(u / 2, u % 2, u);
+            __builtin_amdgcn_sched_barrier(0);  // (in this order: the waits below count on it)
         }
         static_assert(S == 2 * D && 4 % D == 0, "every round has the rings' places alike");
         for (int s0 = 0; s0 < stages; s0 += 4) {
@@ -322,7 +323,8 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
                 // This unit's activations have landed here once at most the loads
                 // of the S - 2 units after them are in flight (and the weights of
                 // every other one), and in every wave behind the barrier, where
-                // all are done with the unit before.
+                // all are done with the unit before. (In whichever order a step's
+                // loads are issued, no fewer than these are younger.)
                 wait_vmcnt<(S - 2) * MT + (S - 2) / 2 * 2 * NF>();
                 lds_barrier();
                 if (u == 0) {
@@ -333,7 +335,6 @@ __global__ __launch_bounds__(kThreads, 2) void moe_tile_kernel(const MoeGemmArgs
                     load_w(s + D - 1, (u / 2 + D - 1) % D);
                 const int next = u + S - 1;
                 load_x(s0 + next / 2, next % 2, next % S);
-                __builtin_amdgcn_sched_barrier(0);  // (loads first, then what waits)
                 uint32_t sc[NF];
 #pragma unroll
                 for (int f = 0; f < NF; ++f)
