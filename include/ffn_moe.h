@@ -126,9 +126,9 @@ int ffn_moe_gemm(const void *x, int x_rows, int dtype, const int32_t *rows, int 
  * initialisation. */
 size_t ffn_moe_workspace_bytes(int T, int top_k, int E, int K, int N);
 
-/* The whole sparse FFN (formula above). h is rounded to `dtype` once, as is
- * each expert's output before the weighted sum, which runs in fp32 with j
- * ascending.
+/* The whole sparse FFN (formula above). h is rounded to `dtype` once; the
+ * experts' outputs stay in fp32 until their weighted sum, which runs with j
+ * ascending, is rounded.
  *   x          device [T, K] of `dtype` (FFN_MOE_BF16 or FFN_MOE_F16)
  *   ids        device int32 [T, top_k]; weights: device fp32 [T, top_k]
  *   gate, up   host structs of weights [N, K]; down: of weights [K, N]

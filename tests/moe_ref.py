@@ -88,11 +88,10 @@ def forward(x, ids, weights, gate, up, down, act):
         a = act_of(g, act)
         h = a * u
         hb = 1.13 * gb * (u.abs() + ub) + a.abs() * ub + act_bound(g, act) * h.abs() + 2 * U * h.abs()
-        hb = hb + half(t) * (h.abs() + hb) + torch.finfo(t).tiny  # h's rounding
+        hb = hb + half(t) * (h.abs() + hb) + torch.finfo(t).tiny  # h's rounding, the only one to 16 bits before the result's
         d = dense(down, e)
         y = h @ d.t()
         yb = hb @ d.abs().t() + (h.shape[1] + 2) * U * ((h.abs() + hb) @ d.abs().t())
-        yb = yb + half(t) * (y.abs() + yb) + torch.finfo(t).tiny  # and y's
         p = weights[tok, j].double()[:, None]
         out.index_add_(0, tok, p * y)
         bound.index_add_(0, tok, p.abs() * yb)

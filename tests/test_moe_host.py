@@ -94,7 +94,7 @@ def test_types_and_values():
 
 def test_workspace():
     need = ffn.moe_workspace_bytes(3, 2, 16, 256, 512)
-    assert need >= 6 * 2 * (256 + 512)
+    assert need >= 6 * (4 * 256 + 2 * 512)
     assert fwd(T=3, wsb=need - 1) == ffn.ERR_WORKSPACE
     need = ffn.moe_plan_workspace_bytes(65536, 8, 256)
     assert need > 0 and plan(T=65536, k=8, E=256, wsb=need - 1) == ffn.ERR_WORKSPACE

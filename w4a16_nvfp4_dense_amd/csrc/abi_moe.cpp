@@ -66,8 +66,8 @@ ffn::MoeWeightArg weight(const ffn_moe_weight *w)
     return ffn::MoeWeightArg{w->codes, w->scales, w->scale2};
 }
 
-// The workspace of the whole FFN: the plan, h [R, N] and the experts' outputs
-// y [R, K], both of two bytes an element, R = T * top_k.
+// The workspace of the whole FFN: the plan, h [R, N] of two bytes an element and
+// the experts' outputs y [R, K] in fp32, R = T * top_k.
 struct Workspace {
     size_t rows, offsets, places, plan, h, y, total;
 };
@@ -82,7 +82,7 @@ Workspace layout(int T, int top_k, int E, int K, int N)
     w.plan = w.places + round256(4 * R);
     w.h = w.plan + round256(ffn::moe_plan_workspace(static_cast<int>(R), E));
     w.y = w.h + round256(2 * R * N);
-    w.total = w.y + round256(2 * R * K);
+    w.total = w.y + round256(4 * R * K);
     return w;
 }
 
@@ -213,10 +213,10 @@ int ffn_moe_forward(const void *x, int T, int K, int N, int E, int top_k, int dt
     const ffn::MoeGemmArgs first{x, rows, offsets, slots, weight(gate), weight(up), ws + w.h, T, top_k, R, E, K, N};
     const ffn::MoeGemmArgs last{ws + w.h, nullptr, offsets, slots, weight(down), {}, ws + w.y, R, 1, R, E, N, K};
     if ((e = ffn::launch_moe_gemm(first, dtype, gated, stream)) != hipSuccess ||
-        (e = ffn::launch_moe_gemm(last, dtype, ffn::MOE_SAME, stream)) != hipSuccess)
+        (e = ffn::launch_moe_gemm(last, dtype, ffn::MOE_F32, stream)) != hipSuccess)
         return FFN_NVFP4_ERR_LAUNCH;
     return launch_status(
-        ffn::launch_moe_combine(ws + w.y, places, slots, weights, T, top_k, R, E, K, dtype, out, stream));
+        ffn::launch_moe_combine(reinterpret_cast<const float *>(ws + w.y), places, slots, weights, T, top_k, R, E, K, dtype, out, stream));
 }
 
 }  // extern "C"

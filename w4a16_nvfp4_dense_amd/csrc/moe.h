@@ -28,11 +28,11 @@ size_t moe_plan_workspace(int R, int E);
 hipError_t launch_moe_plan(const int32_t *ids, int R, int E, int32_t *rows, int32_t *offsets, int32_t *places,
                            void *workspace, hipStream_t stream);
 
-// out[t] = sum_j weights[t, j] * y[places[t, j]] (moe_combine.hip), y and out
-// of `dtype` with K columns, K a multiple of 8; places outside 0 .. R - 1 are
+// out[t] = sum_j weights[t, j] * y[places[t, j]] (moe_combine.hip), y in fp32 and
+// out of `dtype` with K columns, K a multiple of 8; places outside 0 .. R - 1 are
 // skipped. With `ids` in place of places, y has a row for each slot; slots with
 // ids outside 0 .. E - 1 are skipped.
-hipError_t launch_moe_combine(const void *y, const int32_t *places, const int32_t *ids, const float *weights, int T,
+hipError_t launch_moe_combine(const float *y, const int32_t *places, const int32_t *ids, const float *weights, int T,
                               int top_k, int R, int E, int K, int dtype, void *out, hipStream_t stream);
 
 struct MoeWeightArg {

@@ -437,7 +437,7 @@ hipError_t launch_out(const MoeGemmArgs &a, hipStream_t stream)
 template <class T, int OUT>
 hipError_t launch_either(const MoeGemmArgs &a, hipStream_t stream)
 {
-    if constexpr (OUT != MOE_F32)
+    if constexpr (OUT != MOE_SAME)
         if (a.ids)
             return launch_moe_stream<T, true, OUT>(a, stream);
     return launch_out<T, OUT>(a, stream);
