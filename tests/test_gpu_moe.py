@@ -210,6 +210,43 @@ def test_gemm_reads_rows_where_they_are(T, k, E):
     assert torch.equal(a, b)
 
 
+# Shapes that reach each of the kernels' variants: the stream of few rows, one tile of many experts' rows after
+# another; tiles of 32, 64 and 128 rows, where there are enough of them for the device and where there are not.
+VARIANTS = [
+    ([40] + [0] * 9, 64, 700), ([100, 1, 0, 17] + [0] * 20, 160, 96), ([512] + [0] * 40, 256, 48),
+    ([20, 31, 1, 17, 18], 672, 3000), ([40, 64, 31, 50], 160, 16500), ([25, 96, 33, 64], 288, 16384),
+    ([200, 129, 33, 300], 96, 8192), ([70, 128, 1, 97], 160, 16501), ([64, 65, 129, 257], 672, 9000),
+    ([70, 128, 1, 97], 224, 130), ([1000], 416, 700), ([90] * 40, 128, 513),
+]
+
+
+@pytest.mark.parametrize("counts,K,N", VARIANTS, ids=lambda v: str(v)[:24])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("wide", [False, True])
+def test_gemm_variants(counts, K, N, dtype, wide):
+    R = sum(counts)
+    w = ref.experts(len(counts), N, K, R + N)
+    x = torch.randn(R, K, generator=gen(R), device=DEV).to(dtype)
+    out = check_gemm(x, by_counts(counts), w, out_dtype=F if wide else None)
+    x[R // 2] = math.nan
+    again = ffn.moe_gemm(x, by_counts(counts), w, out_dtype=F if wide else None)
+    keep = torch.arange(R, device=DEV) != R // 2
+    assert torch.isnan(again[R // 2]).all() and torch.equal(again[keep], out[keep])
+
+
+@pytest.mark.parametrize("T,E,k,K,N", [(400, 4, 1, 96, 8192), (300, 4, 2, 160, 4128), (130, 3, 1, 288, 12000),
+                                       (64, 64, 8, 96, 64), (600, 1, 1, 32, 64)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_forward_variants(T, E, k, K, N, dtype):
+    ws = layer(E, K, N, T)
+    x = torch.randn(T, K, generator=gen(T), device=DEV).to(dtype)
+    ids = torch.randint(-1, E, (T, k), generator=gen(T + 1), device=DEV, dtype=torch.int32)
+    p = torch.rand(T, k, generator=gen(T + 2), device=DEV)
+    check_forward(x, ids, p, ws)
+    ids[:] = E - 1  # one expert has all
+    check_forward(x, ids, p, ws, ffn.ACT_GELU_TANH)
+
+
 def test_gemm_rows_outside_all_experts_are_left():
     w = ref.experts(3, 64, 128, 1)
     x = torch.randn(100, 128, generator=gen(2), device=DEV).to(BF)
@@ -225,6 +262,10 @@ def test_gemm_offsets_and_rows_out_of_range_stay_inside():
     room = torch.full((50 + 64, 64), -77.0, dtype=BF, device=DEV)
     for off in ([-5, 10, 2 ** 31 - 1, 7], [-(2 ** 31), 2 ** 31 - 1, 0, 50], [50, 40, 30, 20]):
         ffn.moe_gemm(x, torch.tensor(off, device=DEV, dtype=torch.int32), w, out=room[:50])
+        assert (room[50:] == -77).all()
+    many = ref.experts(1000, 64, 128, 1)  # every expert but the last claims all rows, or half of them do
+    for off in ([0, 50] * 500 + [50], [0] * 500 + [50] * 501):
+        ffn.moe_gemm(x, torch.tensor(off, device=DEV, dtype=torch.int32), many, out=room[:50])
         assert (room[50:] == -77).all()
     rows = torch.tensor([-1, 2 ** 31 - 1, 0, -(2 ** 31)] * 8, device=DEV, dtype=torch.int32)
     out = ffn.moe_gemm(x, torch.tensor([0, 10, 20, 32], device=DEV, dtype=torch.int32), w, rows=rows, top_k=3)
@@ -485,6 +526,10 @@ def test_past_4_gib_of_weights_activations_and_outputs():
     y, b = ref.gemm(x[-130:].contiguous(), by_counts([125, 5]), w)
     ref.within(out[-130:], y, b)
     assert (out[:-130] == 0).all()
+    # tokens' rows read where they are, some of them past 2^32 bytes
+    rows = torch.randint(3 * (R - 130), 3 * R, (200,), generator=gen(7), device=DEV, dtype=torch.int32)
+    check_gemm(x, by_counts([150, 50]), w, rows=rows, top_k=3)
+    check_gemm(x, by_counts([20, 3]), w, rows=rows[:23].contiguous(), top_k=3)
     del x, out
     N = 32768
     w = ref.experts(2, N, 32, 5)
