@@ -247,6 +247,34 @@ def test_forward_variants(T, E, k, K, N, dtype):
     check_forward(x, ids, p, ws, ffn.ACT_GELU_TANH)
 
 
+# Reductions past what a workgroup's registers hold, which go block by block: whole blocks, a last one of 64 columns
+# and of others, several tiles of an expert, one weight row.
+@pytest.mark.parametrize("K,N", [(5632, 96), (6080, 31), (6208, 33), (8192, 130), (10304, 1), (14336, 512), (14400, 95), (65536, 17)])
+@pytest.mark.parametrize("counts", [[1], [0, 1, 16, 0, 3], [17, 0, 2, 33] + [0] * 4, [1] * 20 + [40]],
+                         ids=lambda c: "_".join(map(str, c[:4])))
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_gemm_reductions_in_blocks(counts, K, N, dtype):
+    R = sum(counts)
+    w = ref.experts(len(counts), N, K, R + N)
+    x = torch.randn(R, K, generator=gen(R + K), device=DEV).to(dtype)
+    out = check_gemm(x, by_counts(counts), w, out_dtype=F if N % 2 else None)
+    x[R // 2, K - 1] = math.nan
+    again = ffn.moe_gemm(x, by_counts(counts), w, out_dtype=F if N % 2 else None)
+    keep = torch.arange(R, device=DEV) != R // 2
+    assert torch.isnan(again[R // 2]).all() and torch.equal(again[keep], out[keep])
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (3, 3, 3), (40, 8, 2), (255, 40, 2), (300, 64, 3)])
+@pytest.mark.parametrize("K,N", [(512, 14336), (5696, 6144), (8256, 160), (6208, 6272)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_forward_reductions_in_blocks(T, E, k, K, N, dtype):
+    ws = layer(E, K, N, T)
+    x = torch.randn(T, K, generator=gen(T), device=DEV).to(dtype)
+    ids = torch.randint(-1, E, (T, k), generator=gen(T + 1), device=DEV, dtype=torch.int32)
+    p = torch.rand(T, k, generator=gen(T + 2), device=DEV)
+    check_forward(x, ids, p, ws)
+
+
 def test_gemm_rows_outside_all_experts_are_left():
     w = ref.experts(3, 64, 128, 1)
     x = torch.randn(100, 128, generator=gen(2), device=DEV).to(BF)

@@ -215,8 +215,8 @@ int ffn_moe_forward(const void *x, int T, int K, int N, int E, int top_k, int dt
     if ((e = ffn::launch_moe_gemm(first, dtype, gated, stream)) != hipSuccess ||
         (e = ffn::launch_moe_gemm(last, dtype, ffn::MOE_F32, stream)) != hipSuccess)
         return FFN_NVFP4_ERR_LAUNCH;
-    return launch_status(
-        ffn::launch_moe_combine(reinterpret_cast<const float *>(ws + w.y), places, slots, weights, T, top_k, R, E, K, dtype, out, stream));
+    return launch_status(ffn::launch_moe_combine(reinterpret_cast<const float *>(ws + w.y), places, slots, weights, T,
+                                                 top_k, R, E, K, dtype, out, stream));
 }
 
 }  // extern "C"

@@ -14,14 +14,27 @@
 // XCDs in runs, so that an XCD's L2 holds what its tiles share.
 //
 // A workgroup has four waves; each dequantises 64 weight rows of the tile (32
-// of either weight) and multiplies them with all its rows. Columns go by units
-// of 64; in step t (of four) of a unit, lane half h = lane / 32 holds columns
-// 32 h + 8 t .. + 7 of either operand.
+// of either weight) and multiplies them with all its rows. Activations come
+// through a ring of LDS units of 64 columns, by direct loads of 16 bytes a lane,
+// the pieces swizzled so that reads meet no bank twice (none counted). Codes and
+// scales are used by one wave only, so they come to registers, by stages of 128
+// columns: lane half h = lane / 32 has columns 64 h .. + 63, two 16-byte pieces, and
+// unit v of a stage is columns 64 h + 32 v .. + 31 of either half; in step t (of
+// four) of a unit a lane multiplies eight of them. One barrier a unit.
 //
-// Activations and codes come through a ring of LDS stages of one unit each, by
-// direct loads of 16 bytes a lane, the 16-byte pieces swizzled so that reads meet
-// no bank twice; the two scale bytes that a lane needs of a unit come to
-// registers, as long ahead. One barrier a unit.
+// What bounds it. Many rows of an expert: the matrix cores, at the clock that
+// the card's power leaves. 4019 tokens, 8 of 64 experts each, 5120/2048: gate and up
+// 1.35 TFLOP in 1300 - 1391 us, 970 - 1037 TFLOP/s; down 674 GFLOP in 706 - 750, 899 -
+// 955; 16384 rows of 64 experts, 5120 -> 2048: 343.6 GFLOP in 375 - 405 us, 848 - 916.
+// A large bf16 library product reaches 1450. The matrix cores are busy 51 -
+// 57% of the time; with operands of zeros, so at the full clock, the same kernel
+// does 1697 TFLOP/s, without its reads of LDS it is 17% faster, with all weights in
+// L2 10%. Tiles of 512 channels and eight waves (half the reads of activations
+// from L2): 2213 us for 2172 of the whole layer; channels fastest instead of rows:
+// 2229. Few rows: the weights' way in, a tile's worth of latency; two groups of
+// waves that share the columns of a tile: 49.9 us for 48.4 at 777 rows of 17
+// experts. Weights through LDS as well, in pieces of 32 bytes a row: 172 us for 134
+// at 32 rows each of 64 experts, 5120 -> 2048.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -418,11 +431,31 @@ hipError_t launch_tiles(const MoeGemmArgs &a, hipStream_t stream)
 template <class T, int OUT>
 hipError_t launch_out(const MoeGemmArgs &a, hipStream_t stream)
 {
-    if (a.R <= kStreamRows * a.E && stream_fits(a.E, a.K, a.N))
+    // Which kernel, by the mean rows of an expert; us at experts x rows, K -> N (of
+    // two weights: "dual"):
+    //                              few rows  32 x 256  64 x 256  128 x 256
+    //   64 x 16, 5120 -> 2048            92       116
+    //   64 x 16, 2048 -> 5120            88       101
+    //   128 x 16, dual 2048 -> 1024      71        83
+    //   64 x 20, 5120 -> 2048                     121       116       131
+    //   64 x 32, 5120 -> 2048           151       118       123       132
+    //   128 x 32, dual 2048 -> 1024     105        88        95       103
+    //   64 x 48, 5120 -> 2048                     190       137       142
+    //   64 x 64, 5120 -> 2048                     199       140       154
+    //   128 x 64, dual 2048 -> 1024               156       109       118
+    //   64 x 96, 5120 -> 2048                     261       223       200
+    //   128 x 96, dual 2048 -> 1024               217       188       162
+    // (64-row tiles need two 32-row fragments of sums where rows pass 32 at random,
+    // as they do from a mean of about 24 on). Where the large tiles are fewer than
+    // the compute units, smaller ones: 8 x 200, 2048 -> 1024: 34.7 us with 128 x 256,
+    // 24.9 with 64 x 256, 20.6 with 64 x 128, 21.0 with 32 x 128; 64 x 128, 2048 ->
+    // 5120, which has enough: 207 with 128 x 256, 227 with 128 x 128.
+    if (stream_fits<moe_two_weights(OUT)>(a.R, a.E, a.K, a.N))
         return launch_moe_stream<T, false, OUT>(a, stream);
+    // (rows of x past 32-bit offsets: a 64-row variant only)
     if (a.rows && static_cast<uint64_t>(a.x_rows) * a.K * 2 >= kPast)
         return launch_tiles<T, 2, 2, OUT, true>(a, stream);
-    const int mean = a.R / a.E, cus = device_cu_count();  // rows of an expert
+    const int mean = a.R / a.E, cus = device_cu_count();
     constexpr int BN = tile_channels<2, OUT>();
     if (mean > 64 && most_tiles(a, 128, BN) >= cus)
         return launch_tiles<T, 4, 2, OUT>(a, stream);
@@ -462,7 +495,7 @@ hipError_t launch_type(const MoeGemmArgs &a, MoeOut out, hipStream_t stream)
 
 bool moe_by_slots(int R, int E, int K, int N)
 {
-    return R <= kStreamSlots && R <= kStreamRows * E && stream_fits(E, K, N) && stream_fits(E, N, K);
+    return R <= kStreamSlots && stream_fits<true>(R, E, K, N) && stream_fits<false>(R, E, N, K);
 }
 
 hipError_t launch_moe_gemm(const MoeGemmArgs &a, int dtype, MoeOut out, hipStream_t stream)

