@@ -337,6 +337,30 @@ def test_gemm_every_code_and_scale():
         assert torch.equal(one[0].double(), ref.dense(w, 0)[:, 7])
 
 
+@pytest.mark.parametrize("m", [3, 50, 300])
+def test_gemm_values_below_the_smallest_normal_one(m):
+    """f16 rows of multiples of 2^-24 below 2^-14 keep their value, and so do such results: off by half a step of
+    2^-24 beside the sum's own bound."""
+    w = ref.experts(1, 96, 128, m)
+    x = (torch.randint(-1000, 1001, (m, 128), generator=gen(m), device=DEV).double() * 2.0 ** -24).to(HF)
+    y, b = ref.gemm(x, by_counts([m]), w)
+    assert (y.abs() > 2.0 ** -20).any()
+    out = ffn.moe_gemm(x, by_counts([m]), w, out_dtype=F)
+    ref.within(out, y, b)
+    out = ffn.moe_gemm(x, by_counts([m]), w)
+    ref.within(out, y, b + (half(HF) * (y.abs() + b)).clamp_min(2.0 ** -25))
+
+
+@pytest.mark.parametrize("T", [2, 300])
+def test_forward_of_one_expert_that_all_tokens_name(T):
+    """A router that has collapsed: many experts, all rows with a few of them."""
+    ws = layer(96, 192, 128, T)
+    x = torch.randn(T, 192, generator=gen(T), device=DEV).to(BF)
+    ids = torch.tensor([[95, 3, 3]], device=DEV, dtype=torch.int32).repeat(T, 1)
+    p = torch.rand(T, 3, generator=gen(T + 1), device=DEV)
+    check_forward(x, ids, p, ws)
+
+
 # ------------------------------------------------------------------- the layer
 
 
