@@ -592,3 +592,17 @@ def test_past_4_gib_of_weights_activations_and_outputs():
     ref.within(out[-130:], y, b + half(BF) * (y.abs() + b))
     y, b = ref.gemm(x[:100].contiguous(), by_counts([100, 0]), w)
     ref.within(out[:100], y, b + half(BF) * (y.abs() + b))
+
+
+@pytest.mark.parametrize("x_rows", [40000, 57000, 57400])
+def test_tokens_rows_at_the_ends_of_32_bit_offsets(x_rows):
+    # 2.6e9 bytes; a little under and over the 3.75e9 up to which rows are gathered with 32-bit offsets
+    K = 32768
+    w = ref.experts(2, 160, K, 3)
+    x = torch.zeros(x_rows, K, dtype=HF, device=DEV)
+    x[:30] = torch.randn(30, K, generator=gen(4), device=DEV)
+    x[-30:] = torch.randn(30, K, generator=gen(5), device=DEV)
+    rows = torch.randint(-60, 60, (200,), generator=gen(7), device=DEV, dtype=torch.int32)
+    rows = torch.where(rows < 0, rows + 2 * x_rows, rows)
+    check_gemm(x, by_counts([150, 50]), w, rows=rows, top_k=2)
+    check_gemm(x, by_counts([20, 3]), w, rows=rows[:23].contiguous(), top_k=2)
