@@ -81,6 +81,10 @@ typedef struct ffn_moe_weight {
  *     fewer than top_k are, the ids behind them are -1, their weights 0.
  *   - A NaN logit ranks below every number but is available; weights are what
  *     the formula gives.
+ *   - That holds where the scores alone are out of range too: logits of -88 and
+ *     -89, or -1000 and -1001, have normalised sigmoid weights of 0.73 and 0.27.
+ *     Only the sigmoid of the type's lowest finite value, which masks put in,
+ *     counts as 0.
  *   logits   device [T, E] of `dtype`
  *   bias     device fp32 [E], or NULL
  *   scale    finite (else FFN_NVFP4_ERR_SCALE2)

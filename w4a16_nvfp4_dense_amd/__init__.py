@@ -1063,7 +1063,9 @@ def moe_route(logits, top_k: int, score: int = SCORE_SOFTMAX, bias=None, normali
     the lower expert, and their weights ``scale * score`` (``normalize``: over
     the sum of the chosen scores). The key is the logit, or with ``bias`` (fp32
     [E]) score + bias. Experts with a logit or key of -infinity are not
-    chosen: an id of -1 with weight 0 stands where too few are left."""
+    chosen: an id of -1 with weight 0 stands where too few are left. Weights
+    hold where scores are out of range too; the sigmoid of the type's lowest
+    finite value, a mask's, counts as 0."""
     import torch
     T, E = logits.shape
     dev = logits.device

@@ -12,11 +12,13 @@
 //
 // Logits are read once, and a token's choices never leave its wave. Vector
 // instructions bound it (top_k maxima one after another): 16384 tokens of 256
-// experts, bf16, top 8, 11.9 us, where its 9.4 MB are 2; 333 tokens of 160 experts
-// with 64-bit scores 5.5; one token a launch, 2.1.
+// experts, top 8, bf16 11.6 us, where the 9.4 MB are 2, fp32 15.5, with a bias (E
+// exponentials of 64 bits for each token) 24 - 26; 333 tokens of 160 experts, fp32
+// with a bias 5.3; one token a launch, 2.2, with a bias 3.3.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "int8_device.h"
 #include "moe.h"
@@ -91,6 +93,57 @@ __device__ __forceinline__ float logit(const void *p, size_t i)
     return static_cast<float>(static_cast<const L *>(p)[i]);
 }
 
+// 1 / (1 + e^-l); where that e^-l may be infinite e^l, the same number.
+__device__ __forceinline__ double logistic(float l)
+{
+    const bool low = l < -700.0f;
+    const double z = exp(static_cast<double>(low ? l : -l));
+    return low ? z : 1.0 / (1.0 + z);
+}
+
+__device__ __forceinline__ float wave_most(float v)
+{
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2)
+        v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+
+// The weight of lane j's choice (`there`: it has one), of logit l and a sigmoid
+// score: scale * score, `normalize`: over the sum of the wave's choices. S: float where
+// 32 bits do, which is not so far below 0: there every score is 0 from -89 on, and
+// the sum with them, while their quotients are as good as any. So such choices have
+// 64 bits, and where all of them are below -40 (a score is e^l to 2^-57 of it), the
+// scores of a quotient are times e^-(the largest logit): 64 bits alone end at -745.
+// The type's lowest value is what masks put in: its score is 0.
+template <class L, class S>
+__device__ __forceinline__ float logistic_weight(float l, bool there, bool normalize, float scale)
+{
+    if (sizeof(S) == 4 && !__any(there && l < -80.0f)) {
+        float weight = there ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+        if (normalize) {
+            const float sum = from_lane(segment_sum<64>(weight), 63);
+            weight = sum == 0.0f ? 0.0f : weight / sum;
+        }
+        return weight * scale;
+    }
+    constexpr float lowest = std::is_same<L, float>::value    ? -3.40282347e38f
+                             : std::is_same<L, __bf16>::value ? -3.38953139e38f
+                                                              : -65504.0f;
+    double weight;
+    if (normalize && !__any(there && !(l < -40.0f)))
+        weight = exp(static_cast<double>(l) - static_cast<double>(wave_most(there ? l : -INFINITY)));
+    else
+        weight = logistic(l);
+    if (!there || l == lowest)
+        weight = 0.0;
+    if (normalize) {
+        const double sum = wave_sum_all(weight);
+        weight = sum == 0.0 ? 0.0 : weight / sum;
+    }
+    return static_cast<float>(weight * scale);
+}
+
 // PER: experts of a lane. S: the type of scores and keys (double with a bias).
 template <class L, class S, int PER>
 __global__ __launch_bounds__(kTokens * 64) void moe_route_kernel(const MoeRouteArgs a)
@@ -100,7 +153,6 @@ __global__ __launch_bounds__(kTokens * 64) void moe_route_kernel(const MoeRouteA
     const int t = blockIdx.x * kTokens + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (t >= a.T)
         return;
-    S score[PER];
     Key key[PER];
     float l[PER];
     float most = -INFINITY;
@@ -108,17 +160,13 @@ __global__ __launch_bounds__(kTokens * 64) void moe_route_kernel(const MoeRouteA
     for (int i = 0; i < PER; ++i) {
         const int e = i * 64 + lane;
         l[i] = e < a.E ? logit<L>(a.logits, static_cast<size_t>(t) * a.E + e) : -INFINITY;
+        key[i] = key_of(l[i]);
         most = fmaxf(most, l[i]);
     }
-    if (a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            score[i] = S(1) / (S(1) + exp(-static_cast<S>(l[i])));
-    } else {
-#pragma unroll
-        for (int d = 32; d > 0; d /= 2)
-            most = fmaxf(most, __shfl_xor(most, d));
-        S sum = 0;
+    S sum = 0;  // of a softmax
+    S score[PER];
+    if (!a.sigmoid) {
+        most = wave_most(most);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             // (an expert that is not there adds nothing, whatever `most` is)
@@ -126,19 +174,16 @@ __global__ __launch_bounds__(kTokens * 64) void moe_route_kernel(const MoeRouteA
             sum += score[i];
         }
         sum = wave_sum_all(sum);
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            score[i] /= sum;
     }
+    if constexpr (sizeof(S) == 8) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = i * 64 + lane;
-        key[i] = key_of(l[i]);
-        if constexpr (sizeof(S) == 8)
-            key[i] = e < a.E && l[i] != -INFINITY ? key_of(score[i] + static_cast<S>(a.bias[e])) : Key(0);
+        for (int i = 0; i < PER; ++i) {
+            const int e = i * 64 + lane;
+            const S s = a.sigmoid ? logistic(l[i]) : score[i] / sum;
+            key[i] = e < a.E && l[i] != -INFINITY ? key_of(s + static_cast<S>(a.bias[e])) : Key(0);
+        }
     }
-    int id = -1;    // lane j: the token's j-th expert
-    S weight = 0;   // and its score
+    int id = -1;  // lane j: the token's j-th expert
     for (int j = 0; j < a.top_k; ++j) {
         Key best = key[0];
 #pragma unroll
@@ -160,28 +205,45 @@ __global__ __launch_bounds__(kTokens * 64) void moe_route_kernel(const MoeRouteA
             }
         }
         const int first = __ffsll(lanes) - 1;
-        S s = score[0];
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (i == at) {
-                s = score[i];
-                if (lane == first)
-                    key[i] = 0;
-            }
-        s = from_lane(s, first);
-        if (lane == j) {
+            if (i == at && lane == first)
+                key[i] = 0;
+        if (lane == j)
             id = at * 64 + first;
-            weight = s;
-        }
     }
-    if (a.normalize) {
-        const S sum = wave_sum_all(weight);
-        weight = sum == 0 ? S(0) : weight / sum;
+    // The weights, of the chosen logits alone.
+    const bool there = id >= 0;
+    float chosen = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const float v = __shfl(l[i], id & 63);
+        chosen = there && id >> 6 == i ? v : chosen;
+    }
+    float weight;
+    if (a.sigmoid) {
+        weight = logistic_weight<L, S>(chosen, there, a.normalize, a.scale);
+    } else {
+        // A bias may choose experts whose scores all are next to 0, or 0, beside that
+        // of another: the quotients are those of the logits' exponentials. (Without one
+        // the largest of all is among the chosen.)
+        S w = static_cast<S>(chosen) - static_cast<S>(most);
+        const bool apart = sizeof(S) == 8 && a.normalize && !__any(there && !(w < -40));
+        if (apart)
+            w = static_cast<S>(chosen) - static_cast<S>(wave_most(chosen));
+        w = there ? exp(w) : S(0);
+        if (there && (!apart || sum != sum))
+            w /= sum;
+        if (a.normalize) {
+            const S of_chosen = wave_sum_all(w);
+            w = of_chosen == 0 ? S(0) : w / of_chosen;
+        }
+        weight = static_cast<float>(w * static_cast<S>(a.scale));
     }
     if (lane < a.top_k) {
         const size_t o = static_cast<size_t>(t) * a.top_k + lane;
         a.ids[o] = id;
-        a.weights[o] = static_cast<float>(weight * static_cast<S>(a.scale));
+        a.weights[o] = weight;
     }
 }
 
@@ -247,7 +309,7 @@ __global__ __launch_bounds__(kTokens * 64) void moe_route_packed_kernel(const Mo
     const float chosen = packed_logit<L>(mine);
     float weight;
     if (a.sigmoid) {
-        weight = 1.0f / (1.0f + expf(-chosen));
+        weight = logistic_weight<L, float>(chosen, mine != 0, a.normalize, a.scale);
     } else {
         const float most = packed_logit<L>(first);
         float sum = 0.0f;
@@ -255,17 +317,18 @@ __global__ __launch_bounds__(kTokens * 64) void moe_route_packed_kernel(const Mo
         for (int i = 0; i < PER; ++i)
             sum += i * 64 + lane < a.E ? expf(l[i] - most) : 0.0f;
         weight = expf(chosen - most) / from_lane(segment_sum<64>(sum), 63);
-    }
-    if (mine == 0)
-        weight = 0.0f;
-    if (a.normalize) {
-        const float sum = from_lane(segment_sum<64>(weight), 63);
-        weight = sum == 0.0f ? 0.0f : weight / sum;
+        if (mine == 0)
+            weight = 0.0f;
+        if (a.normalize) {
+            sum = from_lane(segment_sum<64>(weight), 63);
+            weight = sum == 0.0f ? 0.0f : weight / sum;
+        }
+        weight *= a.scale;
     }
     if (lane < a.top_k) {
         const size_t o = static_cast<size_t>(t) * a.top_k + lane;
         a.ids[o] = mine ? static_cast<int>(0xFFFFu - (mine & 0xFFFFu)) : -1;
-        a.weights[o] = weight * a.scale;
+        a.weights[o] = weight;
     }
 }
 
