@@ -73,6 +73,26 @@ def test_sigmoid_times_a_large_factor(dtype, with_bias):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF, F])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_softmax_times_a_large_factor(dtype, normalize, with_bias):
+    """The same of a softmax whose largest logit is far above the others (of 2^100 e^-110 among them)."""
+    E, k = 70, 6
+    logits = (-110 + 15 * torch.rand(50, E, generator=gen(5), device=DEV)).to(dtype)
+    logits[:, 33] = 0
+    bias = None
+    if with_bias:
+        bias = 2 + torch.rand(E, generator=gen(6), device=DEV)
+        bias[33] = 9
+    ids, w = ffn.moe_route(logits, k, ffn.SCORE_SOFTMAX, bias=bias, normalize=normalize, scale=2.0 ** 100)
+    key = logits.double() if bias is None else bias.double().expand(logits.shape)
+    assert torch.equal(ids, torch.sort(key, dim=1, descending=True, stable=True).indices[:, :k].int())
+    want = expected(logits, ids, ffn.SCORE_SOFTMAX, normalize, 2.0 ** 100)
+    # the sum of a softmax may be in 32 bits: an exponential (2 U) and a tree of E terms on 64 lanes (2 + 6 additions)
+    assert ((w.double() - want).abs() <= (11 * U + 2.0 ** -40) * want).all(), (w, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F])
 @pytest.mark.parametrize("E,k", [(4, 3), (64, 8), (200, 32)])
 @pytest.mark.parametrize("lo,hi", [(-120, -88), (-709, -700), (-725, -712), (-1500, -800)])
 def test_sigmoid_far_below_zero_with_a_bias(dtype, E, k, lo, hi):

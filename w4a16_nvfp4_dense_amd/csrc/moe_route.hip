@@ -109,24 +109,36 @@ __device__ __forceinline__ float wave_most(float v)
     return v;
 }
 
-// The weight of lane j's choice (`there`: it has one), of logit l and a sigmoid
-// score: scale * score, `normalize`: over the sum of the wave's choices. S: float where
-// 32 bits do, which is not so far below 0: there every score is 0 from -89 on, and
-// the sum with them, while their quotients are as good as any. So such choices have
-// 64 bits, and where all of them are below -40 (a score is e^l to 2^-57 of it), the
-// scores of a quotient are times e^-(the largest logit): 64 bits alone end at -745.
-// The type's lowest value is what masks put in: its score is 0.
+// `normalize`: a choice's weight over the sum of the wave's. (In 32 bits the sum has
+// the order of its kernel, that of fp32 logits or of 16-bit ones.)
+template <class L, class S>
+__device__ __forceinline__ S share(S weight, bool normalize)
+{
+    if (!normalize)
+        return weight;
+    S sum;
+    if constexpr (sizeof(S) == 8 || sizeof(L) == 4)
+        sum = wave_sum_all(weight);
+    else
+        sum = from_lane(segment_sum<64>(weight), 63);
+    return sum == 0 ? S(0) : weight / sum;
+}
+
+// The weight of lane j's choice (`there`: it has one), of logit l: scale * score,
+// `normalize`: over the sum of the wave's choices. S: float where 32 bits do, which
+// is not so far below 0 (of a softmax: below the largest logit): there a score is 0
+// from -104 on, as a sigmoid from -89, while its product with scale, or its quotient
+// by scores as small, is as good as any. So such choices have 64 bits; and where
+// all of them are below -40, the scores of a quotient are times e^-(the largest of
+// their logits), for 64 bits alone end at -745.
+
+// A sigmoid. (Below -40 it is e^l to 2^-57 of it.) The type's lowest value is what
+// masks put in: its score is 0.
 template <class L, class S>
 __device__ __forceinline__ float logistic_weight(float l, bool there, bool normalize, float scale)
 {
-    if (sizeof(S) == 4 && !__any(there && l < -80.0f)) {
-        float weight = there ? 1.0f / (1.0f + expf(-l)) : 0.0f;
-        if (normalize) {
-            const float sum = from_lane(segment_sum<64>(weight), 63);
-            weight = sum == 0.0f ? 0.0f : weight / sum;
-        }
-        return weight * scale;
-    }
+    if (sizeof(S) == 4 && !__any(there && l < -80.0f))
+        return share<L>(there ? 1.0f / (1.0f + expf(-l)) : 0.0f, normalize) * scale;
     constexpr float lowest = std::is_same<L, float>::value    ? -3.40282347e38f
                              : std::is_same<L, __bf16>::value ? -3.38953139e38f
                                                               : -65504.0f;
@@ -135,12 +147,25 @@ __device__ __forceinline__ float logistic_weight(float l, bool there, bool norma
         weight = exp(static_cast<double>(l) - static_cast<double>(wave_most(there ? l : -INFINITY)));
     else
         weight = logistic(l);
-    if (!there || l == lowest)
-        weight = 0.0;
-    if (normalize) {
-        const double sum = wave_sum_all(weight);
-        weight = sum == 0.0 ? 0.0 : weight / sum;
-    }
+    weight = share<L>(there && l != lowest ? weight : 0.0, normalize);
+    return static_cast<float>(weight * scale);
+}
+
+// A softmax; `most`: the largest logit of all, `sum`: that of e^(l - most). (Only a
+// bias chooses experts that are all far below the largest.)
+template <class L, class S>
+__device__ __forceinline__ float softmax_weight(float l, bool there, float most, S sum, bool normalize, float scale)
+{
+    if (sizeof(S) == 4 && !__any(there && l - most < -80.0f))
+        return share<L>(there ? expf(l - most) / static_cast<float>(sum) : 0.0f, normalize) * scale;
+    double weight = static_cast<double>(l) - static_cast<double>(most);
+    const bool apart = normalize && !__any(there && !(weight < -40.0));
+    if (apart)
+        weight = static_cast<double>(l) - static_cast<double>(wave_most(there ? l : -INFINITY));
+    weight = exp(weight);
+    if (!apart || sum != sum)
+        weight /= sum;
+    weight = share<L>(there ? weight : 0.0, normalize);
     return static_cast<float>(weight * scale);
 }
 
@@ -220,26 +245,8 @@ __global__ __launch_bounds__(kTokens * 64) void moe_route_kernel(const MoeRouteA
         const float v = __shfl(l[i], id & 63);
         chosen = there && id >> 6 == i ? v : chosen;
     }
-    float weight;
-    if (a.sigmoid) {
-        weight = logistic_weight<L, S>(chosen, there, a.normalize, a.scale);
-    } else {
-        // A bias may choose experts whose scores all are next to 0, or 0, beside that
-        // of another: the quotients are those of the logits' exponentials. (Without one
-        // the largest of all is among the chosen.)
-        S w = static_cast<S>(chosen) - static_cast<S>(most);
-        const bool apart = sizeof(S) == 8 && a.normalize && !__any(there && !(w < -40));
-        if (apart)
-            w = static_cast<S>(chosen) - static_cast<S>(wave_most(chosen));
-        w = there ? exp(w) : S(0);
-        if (there && (!apart || sum != sum))
-            w /= sum;
-        if (a.normalize) {
-            const S of_chosen = wave_sum_all(w);
-            w = of_chosen == 0 ? S(0) : w / of_chosen;
-        }
-        weight = static_cast<float>(w * static_cast<S>(a.scale));
-    }
+    const float weight = a.sigmoid ? logistic_weight<L, S>(chosen, there, a.normalize, a.scale)
+                                   : softmax_weight<L, S>(chosen, there, most, sum, a.normalize, a.scale);
     if (lane < a.top_k) {
         const size_t o = static_cast<size_t>(t) * a.top_k + lane;
         a.ids[o] = id;
@@ -316,14 +323,8 @@ __global__ __launch_bounds__(kTokens * 64) void moe_route_packed_kernel(const Mo
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             sum += i * 64 + lane < a.E ? expf(l[i] - most) : 0.0f;
-        weight = expf(chosen - most) / from_lane(segment_sum<64>(sum), 63);
-        if (mine == 0)
-            weight = 0.0f;
-        if (a.normalize) {
-            sum = from_lane(segment_sum<64>(weight), 63);
-            weight = sum == 0.0f ? 0.0f : weight / sum;
-        }
-        weight *= a.scale;
+        sum = from_lane(segment_sum<64>(sum), 63);
+        weight = softmax_weight<L, float>(chosen, mine != 0, most, sum, a.normalize, a.scale);
     }
     if (lane < a.top_k) {
         const size_t o = static_cast<size_t>(t) * a.top_k + lane;
