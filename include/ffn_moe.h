@@ -32,7 +32,8 @@
  *   - matrices of values or codes and workspaces are 16-byte aligned, block
  *     scales 2-byte, fp32 and int32 vectors 4-byte (else FFN_NVFP4_ERR_ALIGN)
  *   - an unknown type, activation or score is FFN_NVFP4_ERR_ACT
- *   - outputs and workspaces overlap no other buffer of the call
+ *   - outputs and workspaces overlap no other buffer of the call, unless an
+ *     entry says otherwise (else FFN_NVFP4_ERR_ALIAS)
  * What the device memory of a call holds cannot make it read or write outside
  * its buffers: ids, rows and offsets out of range are left out or taken as the
  * nearest in range.
@@ -139,7 +140,7 @@ size_t ffn_moe_workspace_bytes(int T, int top_k, int E, int K, int N);
  *   workspace  device, >= ffn_moe_workspace_bytes(T, top_k, E, K, N) bytes;
  *              clobbered; calls that share it must not overlap
  *   out        device [T, K] of `dtype` (written; zeros for a token without
- *              an expert) */
+ *              an expert); may be x */
 int ffn_moe_forward(const void *x, int T, int K, int N, int E, int top_k, int dtype, const int32_t *ids,
                     const float *weights, const ffn_moe_weight *gate, const ffn_moe_weight *up,
                     const ffn_moe_weight *down, int act, void *workspace, size_t workspace_bytes, void *out,

@@ -1173,7 +1173,7 @@ def moe_forward(x, ids, weights, gate: MoeDeviceWeight, up: MoeDeviceWeight, dow
                 act: int = ACT_SILU, out=None, workspace=None, stream=None):
     """out[t] = sum_j weights[t, j] * W_d,e (act(W_g,e x[t]) * (W_u,e x[t])),
     e = ids[t, j], for x [T, K] (bfloat16 or float16), ids int32 and weights fp32
-    [T, top_k]; an id outside 0 .. E - 1 adds nothing."""
+    [T, top_k]; an id outside 0 .. E - 1 adds nothing. ``out`` may be x."""
     import torch
     T, K = x.shape
     top_k = ids.shape[1]

@@ -9,8 +9,11 @@
 
 #include "int8.h"
 #include "kernels.h"
+#include "span.h"
 
 namespace {
+
+using ffn::Span;
 
 constexpr int kMaxDim = 65536;
 constexpr int kMaxChannels = 1 << 20;  // of a single product
@@ -76,18 +79,6 @@ size_t round256(size_t b)
 size_t dtype_bytes(int t)
 {
     return t == FFN_INT8_F32 ? 4 : 2;
-}
-
-// A buffer of a call. (A null one overlaps nothing.)
-struct Span {
-    const void *p;
-    size_t bytes;
-};
-
-bool overlap(const Span &a, const Span &b)
-{
-    const uintptr_t i = reinterpret_cast<uintptr_t>(a.p), j = reinterpret_cast<uintptr_t>(b.p);
-    return i && j && i < j + b.bytes && j < i + a.bytes;
 }
 
 ffn::Int8Out out_kind(int dtype)
@@ -175,11 +166,11 @@ int ffn_int8_rmsnorm(const void *x, const void *residual, const void *weight, in
     for (int o = 0; o < 4; ++o) {
         for (int i = 0; i < 3; ++i) {
             const bool in_place = o < 2 && i < 2 && out[o].p == in[i].p;
-            if (!in_place && overlap(out[o], in[i]))
+            if (!in_place && ffn::overlap(out[o], in[i]))
                 return FFN_NVFP4_ERR_ALIAS;
         }
         for (int other = 0; other < o; ++other)
-            if (overlap(out[o], out[other]))
+            if (ffn::overlap(out[o], out[other]))
                 return FFN_NVFP4_ERR_ALIAS;
     }
     const ffn::Int8RowsArgs a{x, residual, weight, M, K, eps, weight_offset, codes, scales, sum_out, y_out};

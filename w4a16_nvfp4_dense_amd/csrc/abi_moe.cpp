@@ -7,8 +7,11 @@
 #include <cstdint>
 
 #include "moe.h"
+#include "span.h"
 
 namespace {
+
+using ffn::Span;
 
 constexpr int kMaxDim = 65536;
 constexpr int kMaxChannels = 1 << 20;  // of a single product
@@ -49,6 +52,22 @@ int check_weight(const ffn_moe_weight *w)
     if (!aligned(w->codes, 16) || !aligned(w->scales, 2) || !aligned(w->scale2, 4))
         return FFN_NVFP4_ERR_ALIGN;
     return FFN_NVFP4_OK;
+}
+
+// The buffers of weights [rows, cols] of E experts.
+struct WeightSpans {
+    Span codes, scales, scale2;
+};
+
+WeightSpans spans(const ffn_moe_weight *w, int E, int rows, int cols)
+{
+    const size_t e = static_cast<size_t>(E) * rows * cols;
+    return {{w->codes, e / 2}, {w->scales, e / 16}, {w->scale2, 4 * static_cast<size_t>(E)}};
+}
+
+size_t dtype_bytes(int t)
+{
+    return t == FFN_MOE_F32 ? 4 : 2;
 }
 
 int launch_status(hipError_t e)
@@ -114,6 +133,10 @@ int ffn_moe_route(const void *logits, int T, int E, int dtype, const float *bias
         return FFN_NVFP4_ERR_NULL;
     if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
         return FFN_NVFP4_ERR_ALIGN;
+    const size_t chosen = 4 * static_cast<size_t>(T) * top_k, experts = static_cast<size_t>(E);
+    if (ffn::any_overlap<2, 2>({{ids, chosen}, {weights, chosen}},
+                               {{logits, T * experts * dtype_bytes(dtype)}, {bias, 4 * experts}}))
+        return FFN_NVFP4_ERR_ALIAS;
     const ffn::MoeRouteArgs a{logits, bias, T, E, top_k, score == FFN_MOE_SIGMOID, normalize != 0, scale, ids, weights};
     return launch_status(ffn::launch_moe_route(a, dtype, stream));
 }
@@ -141,6 +164,11 @@ int ffn_moe_plan(const int32_t *ids, int T, int top_k, int E, int32_t *rows, int
         return FFN_NVFP4_ERR_ALIGN;
     if (workspace_bytes < need)
         return FFN_NVFP4_ERR_WORKSPACE;
+    const size_t slots = 4 * static_cast<size_t>(R);
+    if (ffn::any_overlap<4, 1>(
+            {{rows, slots}, {offsets, 4 * (static_cast<size_t>(E) + 1)}, {places, slots}, {workspace, need}},
+            {{ids, slots}}))
+        return FFN_NVFP4_ERR_ALIAS;
     return launch_status(ffn::launch_moe_plan(ids, R, E, rows, offsets, places, workspace, stream));
 }
 
@@ -164,6 +192,12 @@ int ffn_moe_gemm(const void *x, int x_rows, int dtype, const int32_t *rows, int 
         return FFN_NVFP4_ERR_NULL;
     if (!aligned(x, 16) || !aligned(rows, 4) || !aligned(offsets, 4) || !aligned(out, 16))
         return FFN_NVFP4_ERR_ALIGN;
+    const WeightSpans ws = spans(w, E, N, K);
+    const size_t slots = static_cast<size_t>(R);
+    if (ffn::any_overlap<1, 6>({{out, slots * N * dtype_bytes(out_dtype)}},
+                               {{x, static_cast<size_t>(x_rows) * K * 2}, {rows, 4 * slots},
+                                {offsets, 4 * (static_cast<size_t>(E) + 1)}, ws.codes, ws.scales, ws.scale2}))
+        return FFN_NVFP4_ERR_ALIAS;
     const ffn::MoeGemmArgs a{x, rows, offsets, nullptr, weight(w), {}, out, x_rows, top_k, R, E, K, N};
     return launch_status(
         ffn::launch_moe_gemm(a, dtype, out_dtype == FFN_MOE_F32 ? ffn::MOE_F32 : ffn::MOE_SAME, stream));
@@ -196,6 +230,13 @@ int ffn_moe_forward(const void *x, int T, int K, int N, int E, int top_k, int dt
     const Workspace w = layout(T, top_k, E, K, N);
     if (workspace_bytes < w.total)
         return FFN_NVFP4_ERR_WORKSPACE;
+    // x is read before any of out is written, so out may be x.
+    const size_t hidden = static_cast<size_t>(T) * K * 2, chosen = 4 * static_cast<size_t>(T) * top_k;
+    const WeightSpans g = spans(gate, E, N, K), u = spans(up, E, N, K), d = spans(down, E, K, N);
+    if (ffn::any_overlap<2, 12>({{workspace, w.total}, {out, hidden}},
+                                {{out == x ? nullptr : x, hidden}, {ids, chosen}, {weights, chosen}, g.codes, g.scales,
+                                 g.scale2, u.codes, u.scales, u.scale2, d.codes, d.scales, d.scale2}))
+        return FFN_NVFP4_ERR_ALIAS;
     char *ws = static_cast<char *>(workspace);
     int32_t *rows = reinterpret_cast<int32_t *>(ws + w.rows);
     int32_t *offsets = reinterpret_cast<int32_t *>(ws + w.offsets);
