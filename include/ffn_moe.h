@@ -131,7 +131,8 @@ int ffn_moe_gemm(const void *x, int x_rows, int dtype, const int32_t *rows, int 
  * initialisation. */
 size_t ffn_moe_workspace_bytes(int T, int top_k, int E, int K, int N);
 
-/* The whole sparse FFN (formula above). h is rounded to `dtype` once; the
+/* The whole sparse FFN (formula above). h is rounded to `dtype` once (in f16 a
+ * magnitude past 65504 becomes infinite, and its token's outputs with it); the
  * experts' outputs stay in fp32 until their weighted sum, which runs with j
  * ascending, is rounded.
  *   x          device [T, K] of `dtype` (FFN_MOE_BF16 or FFN_MOE_F16)

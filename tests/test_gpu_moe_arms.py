@@ -156,3 +156,22 @@ def test_forward_of_tokens_past_32_bit_offsets(dtype):
     ref.within(out[some], *ref.forward(x[some], ids[some], p[some], *ws, ffn.ACT_SILU))
     out[some] = 0
     assert not out.any()
+
+
+@pytest.mark.parametrize("T", [1, 30, 200])
+def test_h_past_the_range_of_f16(T):
+    """|h| above 65504 is infinite in f16 and its token's outputs with it, no other's; in bf16 it is in range."""
+    E, K, N = 3, 96, 128
+    ws = layer(E, K, N, 9)
+    x = torch.randn(T, K, generator=gen(10), device=DEV)
+    ids = torch.randint(0, E, (T, 2), generator=gen(11), device=DEV, dtype=torch.int32)
+    p = torch.rand(T, 2, generator=gen(12), device=DEV)
+    loud = T // 2
+    clean = ffn.moe_forward(x.to(HF), ids, p, *ws)
+    x[loud] *= 4000
+    out = ffn.moe_forward(x.to(HF), ids, p, *ws)
+    assert not torch.isfinite(out[loud]).any()
+    out[loud] = clean[loud]
+    assert torch.equal(out, clean)
+    x = x.to(BF)
+    ref.within(ffn.moe_forward(x, ids, p, *ws), *ref.forward(x, ids, p, *ws, ffn.ACT_SILU))

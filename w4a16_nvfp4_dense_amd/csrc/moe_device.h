@@ -15,11 +15,6 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
-// Four bytes at any even address.
-struct __attribute__((packed, aligned(2))) pair16_t {
-    uint32_t both;
-};
-
 // What pieces past the last column are loaded from.
 __device__ const u32x4_t kZeros = {0, 0, 0, 0};
 

@@ -7,14 +7,15 @@
 // the only rounding in a sum is that of the matrix core's fp32 accumulation.
 //
 // Tiles. A tile is 32 MT rows of one expert by 256 weight rows (128 channels of
-// two weights). How many tiles an expert has is known on the device only, so
-// the grid is the most there can be, and each workgroup finds its tile from the
-// offsets (a scan over experts); workgroups past the last tile end at once.
-// Tiles are numbered expert by expert, the rows fastest, and dealt to the eight
-// XCDs in runs, so that an XCD's L2 holds what its tiles share.
+// two weights), or by 128 of one weight where the others would be too few. How many
+// tiles an expert has is known on the device only, so the grid is the most there
+// can be, and each workgroup finds its tile from the offsets (a scan over experts);
+// workgroups past the last tile end at once. Tiles are numbered expert by expert,
+// the rows fastest, and dealt to the eight XCDs in runs, so that an XCD's L2 holds
+// what its tiles share.
 //
-// A workgroup has four waves; each dequantises 64 weight rows of the tile (32
-// of either weight) and multiplies them with all its rows. Activations come
+// A workgroup has four waves; each dequantises 32 NF weight rows of the tile, 64
+// (32 of either weight) or 32, and multiplies them with all its rows. Activations come
 // through a ring of LDS units of 64 columns, by direct loads of 16 bytes a lane,
 // the pieces swizzled so that reads meet no bank twice (none counted). Codes and
 // scales are used by one wave only, so they come to registers, by stages of 128
@@ -27,7 +28,9 @@
 // 1.35 TFLOP in 1300 - 1391 us, 970 - 1037 TFLOP/s; down 674 GFLOP in 706 - 750, 899 -
 // 955; 16384 rows of 64 experts, 5120 -> 2048: 343.6 GFLOP in 375 - 405 us, 848 - 916.
 // A large bf16 library product reaches 1450. The matrix cores are busy 51 -
-// 57% of the time; with operands of zeros, so at the full clock, the same kernel
+// 57% of the time. The vector instructions before the products are a small part of
+// it: in f16, which has half as many, those 16384 rows take 382 us for 402. With
+// operands of zeros, so at the full clock, the same kernel
 // does 1697 TFLOP/s, without its reads of LDS it is 17% faster, with all weights in
 // L2 10%. Tiles of 512 channels and eight waves (half the reads of activations
 // from L2): 2213 us for 2172 of the whole layer; channels fastest instead of rows:
@@ -431,23 +434,28 @@ hipError_t launch_tiles(const MoeGemmArgs &a, hipStream_t stream)
 template <class T, int OUT>
 hipError_t launch_out(const MoeGemmArgs &a, hipStream_t stream)
 {
-    // Which kernel, by the mean rows of an expert; us at experts x rows, K -> N (of
-    // two weights: "dual"):
-    //                              few rows  32 x 256  64 x 256  128 x 256
-    //   64 x 16, 5120 -> 2048            92       116
-    //   64 x 16, 2048 -> 5120            88       101
-    //   128 x 16, dual 2048 -> 1024      71        83
-    //   64 x 20, 5120 -> 2048                     121       116       131
-    //   64 x 32, 5120 -> 2048           151       118       123       132
-    //   128 x 32, dual 2048 -> 1024     105        88        95       103
-    //   64 x 48, 5120 -> 2048                     190       137       142
-    //   64 x 64, 5120 -> 2048                     199       140       154
-    //   128 x 64, dual 2048 -> 1024               156       109       118
-    //   64 x 96, 5120 -> 2048                     261       223       200
-    //   128 x 96, dual 2048 -> 1024               217       188       162
-    // (64-row tiles need two 32-row fragments of sums where rows pass 32 at random,
-    // as they do from a mean of about 24 on). Where the large tiles are fewer than
-    // the compute units, smaller ones: 8 x 200, 2048 -> 1024: 34.7 us with 128 x 256,
+    // Which kernel, by the mean rows of an expert; us at experts x mean rows, bf16,
+    // rows gathered. Three counts each: all experts alike / as random logits choose /
+    // as such logits with a popularity of their own deviation for each expert choose.
+    //                             few rows        32 x 256        64 x 256        128 x 256
+    //   64 x 8,  5120 -> 2048    93/ 98/ 79     107/105/ 84     107/106/ 93     113/114/103
+    //   64 x 16, 5120 -> 2048    92/121/114     104/104/126     108/107/103     116/115/125
+    //   64 x 16, 2048 -> 5120    87/104/ 97      99/100/ 95     102/103/ 97     110/111/100
+    //  128 x 16, 2048 -> 1024    36/ 49/ 47      40/ 41/ 47      41/ 41/ 39      44/ 45/ 49
+    //   64 x 20, 5120 -> 2048   146/148/134     103/103/126     106/106/107     117/116/130
+    //   64 x 24, 5120 -> 2048   151/150/155     105/105/130     107/108/105     117/117/132
+    //   64 x 32, 5120 -> 2048   150/196/189     109/145/162     109/113/146     118/120/147
+    //   64 x 32, 2048 -> 5120   135/175/169     107/139/130     110/113/119     115/121/131
+    //  128 x 32, 2048 -> 1024    57/ 71/ 72      42/ 51/ 57      42/ 45/ 55      44/ 47/ 57
+    //   64 x 64, 5120 -> 2048                   169/202/217     125/168/188     137/154/197
+    //   64 x 96, 5120 -> 2048                   234/261/281     200/203/225     180/176/211
+    //   64 x 128, 2048 -> 5120                  297/329/334     224/260/263     192/245/241
+    // A router's counts scatter, so from a mean of about 24 on many experts need a
+    // second tile of 32 rows. At 16 they need a second one of the stream's 16, and tiles
+    // would be up to a sixth faster there on scattered counts, but slower on even
+    // ones and at 8. Where the large tiles are fewer than the compute units, smaller
+    // ones (from a mean of 25 on; 8 x 20, 4096 -> 2048 would be 25 on 64 x 128 and 23 by
+    // the stream for the 34 of 32 x 256): 8 x 200, 2048 -> 1024: 34.7 us with 128 x 256,
     // 24.9 with 64 x 256, 20.6 with 64 x 128, 21.0 with 32 x 128; 64 x 128, 2048 ->
     // 5120, which has enough: 207 with 128 x 256, 227 with 128 x 128.
     if (stream_fits<moe_two_weights(OUT)>(a.R, a.E, a.K, a.N))

@@ -12,11 +12,14 @@
 //
 // Up to kOnce slots one workgroup does it all. More are cut into chunks of
 // kChunk: a first launch counts the chunks, and in the second each chunk's
-// workgroup adds up the counts of all of them (a few tens of KB from L2), those
-// of earlier chunks apart, instead of a launch between the two.
+// workgroup adds up the counts of all of them, those of earlier chunks apart,
+// instead of a launch between the two. That is chunks^2 E 4 bytes from L2: 4 MB for
+// 131072 slots of 256 experts, 4 GB for 2097152 of 1024.
 //
 // It is bound by launches and latency: 256 slots of 128 experts 3.4 us, 131072 of
-// 256 2.6 + 7.5 us (1.6 MB of ids, rows and places: 0.3 us of memory).
+// 256 2.6 + 7.5 us (1.6 MB of ids, rows and places: 0.3 us of memory); at the largest
+// sizes by the adding up: both launches 17 us for 524288 of 256, 27 of 1024; 78 for
+// 2097152 of 256, 181 of 1024.
 #include <hip/hip_runtime.h>
 
 #include "kernels.h"

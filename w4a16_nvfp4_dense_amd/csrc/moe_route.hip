@@ -46,12 +46,6 @@ __device__ __forceinline__ float from_lane(float v, int lane)
 {
     return __uint_as_float(from_lane(__float_as_uint(v), lane));
 }
-__device__ __forceinline__ double from_lane(double v, int lane)
-{
-    const unsigned long long u = __double_as_longlong(v);
-    return __longlong_as_double(static_cast<unsigned long long>(from_lane(static_cast<uint32_t>(u >> 32), lane)) << 32 |
-                                from_lane(static_cast<uint32_t>(u), lane));
-}
 
 // The largest key of the wave, by lane moves (shuffles through LDS instead: 25 us
 // for 17 at 16384 tokens of 256 experts); of 64 bits the upper halves first.
